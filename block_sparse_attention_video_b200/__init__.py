@@ -10,7 +10,10 @@ Entry points carry the C names: ``fvattn_permute``, ``fvattn_route``,
 ``fvattn_route_noalloc``, ``fvattn_sparse_fwd``, ``fvattn_dense_fwd``,
 ``fvattn_block_importance``, ``fvattn_attention_recall``, ``fvattn_select_topp``, ``fvattn_lvsa_lists``,
 ``fvattn_hilbert_table``, ``fvattn_quantize_v``, ``fvattn_sparse_fwd_fp8v``, ``fvattn_dense_fwd_fp8v``,
-``fvattn_workspace_bytes``, ``fvattn_workspace_status``, ``fvattn_wait_selftest``. ``FVAttnPath`` strings
+``fvattn_workspace_bytes``, ``fvattn_workspace_status``, ``fvattn_wait_selftest``, and the paged 4-bit
+key/value cache in ``kv4.py`` (``fvattn_kv4_append``, ``fvattn_kv4_read``, ``fvattn_kv4_select``,
+``fvattn_kv4_attn``, ``fvattn_kv4_workspace_bytes``, ``KV4Cache``, ``KV4Batch``, ``KV4Path``).
+``FVAttnPath`` strings
 them into the full per-call
 path (route -> permute V -> block-sparse attention -> inverse permute) over
 buffers it allocates once with torch; ``HostPipeline`` runs it over a sequence
@@ -53,6 +56,10 @@ FVATTN_OP_DIAG = 3
 FVATTN_OP_LVSA = 4
 FVATTN_OP_HILBERT = 5
 FVATTN_OP_QUANT_V = 6
+FVATTN_OP_KV4_APPEND = 7
+FVATTN_OP_KV4_READ = 8
+FVATTN_OP_KV4_SELECT = 9
+FVATTN_OP_KV4_ATTN = 10
 
 FVATTN_ORDER_TILES = 0
 FVATTN_ORDER_TABLE = 1
@@ -62,7 +69,9 @@ EXPORTED = ("fvattn_workspace_bytes", "fvattn_permute", "fvattn_route", "fvattn_
             "fvattn_select_topp", "fvattn_lvsa_lists", "fvattn_hilbert_table", "fvattn_quantize_v",
             "fvattn_sparse_fwd_fp8v", "fvattn_dense_fwd_fp8v",
             "fvattn_workspace_status", "fvattn_status_string", "fvattn_wait_selftest",
-            "fvattn_permute_quantize_v", "fvattn_order_lists_by_importance")
+            "fvattn_permute_quantize_v", "fvattn_order_lists_by_importance",
+            "fvattn_kv4_workspace_bytes", "fvattn_kv4_append", "fvattn_kv4_read", "fvattn_kv4_select",
+            "fvattn_kv4_attn")
 
 
 class Grid(ctypes.Structure):
@@ -762,3 +771,7 @@ class HostPipeline:
         end = self._ev()
         end.record(cur)
         return end
+
+
+from .kv4 import (KV4Batch, KV4Cache, KV4Path, fvattn_kv4_append, fvattn_kv4_attn,  # noqa: E402,F401
+                  fvattn_kv4_read, fvattn_kv4_select, fvattn_kv4_workspace_bytes)

@@ -40,6 +40,13 @@
  *                           fused with the block-order permutation
  *   fvattn_sparse_fwd_fp8v, fvattn_dense_fwd_fp8v
  *                           attention with that V (8-bit P.V on the tensor cores)
+ * A paged 4-bit key/value cache for sequences that grow (clips generated chunk by
+ * chunk, streams that grow token by token), with grouped query heads:
+ *   fvattn_kv4_append   quantizes the K and V rows of a call into pages
+ *   fvattn_kv4_read     reads rows of the cache back
+ *   fvattn_kv4_select   the pages each query row attends: the routing rule of
+ *                       fvattn_route (mean keys, softmax, Top-p, Top-k floor) per row
+ *   fvattn_kv4_attn     attention over the whole cache or over the selected pages
  *
  * Conventions (every entry point):
  *   - Tensors are dense, row-major, on the current CUDA device. A token row of
@@ -118,10 +125,15 @@ typedef enum {
   FVATTN_OP_DIAG = 3,     /* fvattn_block_importance, fvattn_attention_recall */
   FVATTN_OP_LVSA = 4,     /* fvattn_lvsa_lists */
   FVATTN_OP_HILBERT = 5,  /* fvattn_hilbert_table */
-  FVATTN_OP_QUANT_V = 6   /* fvattn_quantize_v */
+  FVATTN_OP_QUANT_V = 6,  /* fvattn_quantize_v */
+  FVATTN_OP_KV4_APPEND = 7, /* fvattn_kv4_append, sized by fvattn_kv4_workspace_bytes */
+  FVATTN_OP_KV4_READ = 8,   /* fvattn_kv4_read, likewise */
+  FVATTN_OP_KV4_SELECT = 9, /* fvattn_kv4_select, likewise */
+  FVATTN_OP_KV4_ATTN = 10   /* fvattn_kv4_attn, likewise */
 } fvattn_op;
 
-/* Workspace bytes needed by `op` for these sizes (0 if the sizes are invalid).
+/* Workspace bytes needed by `op` for these sizes (0 if the sizes are invalid,
+ * and for the FVATTN_OP_KV4_* calls, which have a sizing call of their own).
  * The workspace must be 256-byte aligned. Its first 256 bytes hold the status
  * word, cleared at the start of every call that takes it. */
 FVATTN_API size_t fvattn_workspace_bytes(fvattn_op op, int B, int H, int N, int d, int block);
@@ -381,6 +393,120 @@ FVATTN_API fvattn_status fvattn_lvsa_lists(int B, int H, const fvattn_grid* grid
                                            int period, int step, int32_t* kv_idx, int32_t* kv_cnt,
                                            int64_t* head_work, void* workspace,
                                            size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Paged 4-bit key/value cache.
+ *
+ * A cache is a pool of num_pages pages. The page of KV head h in pool slot s is the
+ * record pages[s][h], block * (d + d/8) bytes for `block` tokens:
+ *     K codes  [block][d/2]    two E2M1 codes a byte, the even channel in the low bits
+ *     K scales [block][d/16]   one E4M3 scale for each 16 channels of a token
+ *     V codes  [block][d/2]
+ *     V scales [block][d/16]
+ * (E2M1: sign, 2 exponent bits with bias 1, 1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6.)
+ * A code stands for E2M1(code) * E4M3(scale), times k_scale[h] (v_scale[h]) where given.
+ * Quantization of 16 channels: x = fp32(input) / k_scale[h] (one correctly rounded fp32
+ * division; none without k_scale); scale = the nearest E4M3 to min(max |x| / 6, 448);
+ * code = the nearest E2M1 to x / scale, ties to the even code, at most 6 in magnitude;
+ * codes 0 where scale is 0. Inputs must be finite (an infinity is stored as the largest
+ * value, a NaN as some value).
+ * ksum[s][h][c] (int32) is the sum over a full page's tokens of the stored keys without
+ * k_scale, in units of 2^-10 (every stored value is a whole number of them, so the sum is
+ * exact). It is written by fvattn_kv4_append when the last position of a page is written
+ * and has no meaning before. It may be NULL for callers that never select.
+ * d in {64,128}, block in {64,128}.                                              */
+typedef struct {
+  void* pages;           /* device [num_pages][H][block*(d+d/8)] bytes, 16-byte aligned   */
+  int32_t* ksum;         /* device [num_pages][H][d], 16-byte aligned; may be NULL         */
+  const float* k_scale;  /* device [H], positive and finite; NULL = 1                      */
+  const float* v_scale;  /* device [H], positive and finite; NULL = 1                      */
+  int num_pages, H, d, block;   /* H = KV heads                                            */
+} fvattn_kv4_cache;
+
+/* The sequences of a call. Row r of the call's [rows, heads, d] tensors belongs to the
+ * sequence b with cu[b] <= r < cu[b+1]; rows >= cu[B] belong to none: they are neither
+ * read nor written. Row cu[b] + i stands at position kv_len[b] - (cu[b+1]-cu[b]) + i of
+ * its sequence: the rows are the last ones of the kv_len[b] tokens held, the call's own
+ * among them. Position t lies in page table[b][t / block], slot t % block.
+ * All three arrays are device memory and are read when the call's kernels run, so lengths
+ * may change between the replays of a captured call. What they hold is checked there, each
+ * element where it is used: a position outside [0, max_pages*block), a pool slot outside
+ * [0, num_pages) or cu[B] > rows is skipped or clamped and recorded as
+ * FVATTN_ERR_INVALID_ARG in the workspace. A sequence may have no rows. Two sequences may
+ * share pages that no row of the call writes.                                           */
+typedef struct {
+  const int32_t* table;    /* device [B][max_pages] pool slots                            */
+  const int32_t* kv_len;   /* device [B] tokens held                                      */
+  const int32_t* cu;       /* device [B+1] first row of each sequence, cu[0] = 0, ascending */
+  int B, max_pages;
+  int rows;                /* rows of the call's tensors, >= 0 (0: they may be NULL)     */
+  int max_q;               /* the most rows a sequence has (>= 1): chooses the kernel, results
+                              do not depend on it beyond rounding                         */
+} fvattn_kv4_batch;
+
+/* Workspace bytes of the calls below: op = FVATTN_OP_KV4_*, Hq = query heads (a multiple of
+ * the cache's H; ignored by append and read). Pointers in the structs are not looked at. 0
+ * if the sizes are invalid. 256-byte aligned, status word first, as for the other calls.
+ * One workspace serves one call at a time: calls that overlap on the GPU (two streams, two
+ * captured graphs replayed at once) need one each. */
+FVATTN_API size_t fvattn_kv4_workspace_bytes(fvattn_op op, const fvattn_kv4_cache* cache,
+                                             const fvattn_kv4_batch* batch, int Hq);
+
+/* Quantizes the K and V of the call's rows into the pages at their positions, and writes
+ * ksum of every page whose last position is among them (from the page's codes, older ones
+ * included). k, v [rows, H, d] of dtype BF16 or FP32; k_stride, v_stride = elements from
+ * one row to the next (>= H*d, a multiple of 16 bytes), so that k and v may be columns of a
+ * fused projection. Earlier positions are kept; writing a position again replaces it. */
+FVATTN_API fvattn_status fvattn_kv4_append(const fvattn_kv4_cache* cache, const fvattn_kv4_batch* batch,
+                                           const void* k, const void* v, int64_t k_stride,
+                                           int64_t v_stride, fvattn_dtype dtype, void* workspace,
+                                           size_t workspace_bytes, void* stream);
+
+/* Reads the call's rows back: k_out, v_out [rows, H, d] dense, BF16 or FP32, each the stored
+ * value rounded once to fp32 (the product with k_scale or v_scale) and once to dtype. A row
+ * whose position or page is invalid is written as zeros. */
+FVATTN_API fvattn_status fvattn_kv4_read(const fvattn_kv4_cache* cache, const fvattn_kv4_batch* batch,
+                                         void* k_out, void* v_out, fvattn_dtype dtype, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
+/* The pages that each row attends, per KV head: the rule of fvattn_route on single rows.
+ * q [rows, Hq, d] with q_stride elements from row to row; query head h reads KV head
+ * h / (Hq/H). For a row at position t, its own page o = t / block is always attended; of the
+ * pages j < o (all full), with kbar_j = k_scale * ksum_j / (2^10 * block):
+ *   s_gj = softmax_j(scale * q_g . kbar_j) for each of the Hq/H query heads g,
+ *   I_j  = mean over g of s_gj,
+ *   n_p  = the smallest c such that the c largest I_j sum to >= p (o when p >= 1 or when
+ *          no prefix reaches p),
+ *   the min(o, max(n_p, k_min)) largest are attended (ties: the lower page first).
+ * The arithmetic is 64-bit, so that rounding decides no page that is not tied.
+ * kv_idx [rows, H, max_pages] int32: the attended pages (indexes into the sequence's table
+ * row) ascending at entries [0, cnt), own page last; entries >= cnt are not written.
+ * kv_cnt [rows, H] int32: cnt; 0 for a row whose position is invalid.
+ * 0 < p <= 1, k_min >= 1, max_pages <= 8192, scale > 0, Hq/H <= 64. */
+FVATTN_API fvattn_status fvattn_kv4_select(const fvattn_kv4_cache* cache, const fvattn_kv4_batch* batch,
+                                           const void* q, int64_t q_stride, int Hq, fvattn_dtype dtype,
+                                           float scale, float p, int k_min, int32_t* kv_idx,
+                                           int32_t* kv_cnt, void* workspace, size_t workspace_bytes,
+                                           void* stream);
+
+/* Attention of the call's rows over the cache. q [rows, Hq, d] with q_stride elements from
+ * row to row, out [rows, Hq, d] dense, both of dtype; q and out must not overlap. Query head h
+ * reads KV head h / (Hq/H). A row at position t sees the tokens at positions <= t (causal != 0) or all
+ * kv_len of its sequence (causal == 0), and with lists only those in the pages
+ * kv_idx[row, h, 0..kv_cnt) (layout of fvattn_kv4_select). out = softmax(scale * q . k) . v over the
+ * tokens it sees; a row that sees none gives 0. lse: optional [rows, Hq] fp32 natural-log sum of exp of
+ * the scaled logits (-inf for a row that sees none). Without lists kv_idx and kv_cnt are NULL.
+ * Lists ascend strictly: an entry that is not above the one before it, or lies outside the
+ * sequence's pages, is left out and recorded as FVATTN_ERR_INVALID_ARG.
+ * Stored values enter the products exactly (fp16 holds them); the softmax and all sums are fp32.
+ * BF16: q enters exactly (scaled by a power of two; elements below 2^-24 of a row's largest round to
+ * that grid), P is rounded to fp16. FP32: q and P are split into two fp16 parts each.
+ * scale > 0, Hq/H <= 64. */
+FVATTN_API fvattn_status fvattn_kv4_attn(const fvattn_kv4_cache* cache, const fvattn_kv4_batch* batch,
+                                         const void* q, int64_t q_stride, int Hq, void* out, float* lse,
+                                         fvattn_dtype dtype, float scale, int causal,
+                                         const int32_t* kv_idx, const int32_t* kv_cnt, void* workspace,
+                                         size_t workspace_bytes, void* stream);
 
 /* Synchronizes `stream` and returns the status word that the kernels of the
  * last call using `workspace` recorded (FVATTN_OK if none). */

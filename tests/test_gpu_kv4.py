@@ -1,0 +1,703 @@
+"""GPU: the paged 4-bit key/value cache against its fp64 oracle: codes, page sums and lists
+exactly, attention within bounds derived from its roundings, at the lengths, head layouts,
+strides and masks where it can go wrong; refusals; captured and concurrent calls.
+
+Attention's bound, for a row with weights w, A = sum w |v| per channel, S = max |logit| and
+T = max sum |q||k| scale:
+  a logit's error          e_s = T d 2^-24 (fp32 sums of exact products; the fp32 path's split of q
+                                 leaves 2^-22 of T more) + S 2^-22 (product with the scale, exponent's
+                                 argument, both rounded to fp32)
+  a weight's               2 e_s + 2^-21 (ex2.approx, the quotient) + P's rounding to fp16, 2^-11
+                           (bf16 path; the fp32 path keeps 2^-22)
+  P below fp16's range     rounds to a grid of 2^-24 of a value at most 2^-4 of the row's largest P: at
+                           most N 2^-29 A_max
+  output                   half a step of its type, 2^-8 or 2^-24 relative (and 2^-23 for the products
+                           with 1/l and the head's scale)
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv4_oracle as O
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import block_sparse_attention_video_b200 as F
+
+BF16, FP32 = torch.bfloat16, torch.float32
+
+
+class Case:
+    """A pool filled through fvattn_kv4_append with ragged sequences, and the oracle's copy of it."""
+
+    def __init__(self, kv, rows, H, d, block, seed=0, scaled=False, Hq=None, dtype=BF16, spread=1.0, fill=True):
+        self.g = torch.Generator().manual_seed(seed)
+        self.kv, self.nrow, self.H, self.d, self.block, self.dtype = kv, rows, H, d, block, dtype
+        self.Hq = Hq or H
+        dev = torch.device("cuda")
+        need = [max(1, -(-n // block)) for n in kv]
+        self.max_pages = max(need) + 1
+        slots = sum(need) + 3
+        perm = torch.randperm(slots, generator=self.g)
+        table = torch.full((len(kv), self.max_pages), -7, dtype=torch.int32)   # never to be read behind the end
+        at = 0
+        for b, n in enumerate(need):
+            table[b, :n] = perm[at:at + n]
+            at += n
+        self.table_np = table.numpy()
+        sc = lambda: (0.3 + torch.rand(H, generator=self.g)) if scaled else None
+        self.ks, self.vs = sc(), sc()
+        up = lambda t: None if t is None else t.to(dev)
+        self.cache = F.KV4Cache(slots, H, d, block, dev, k_scale=up(self.ks), v_scale=up(self.vs))
+        self.cache.pages.fill_(0x77)                        # what was never written is large
+        self.table = table.to(dev)
+        rnd = lambda n: spread * torch.randn((n, H, d), generator=self.g)
+        self.k = [rnd(n).to(dtype) for n in kv]
+        self.v = [rnd(n).to(dtype) for n in kv]
+        self.batch = self.batch_of(rows)
+        self.rows = sum(rows)
+        if fill:
+            self.append(kv)
+
+    def batch_of(self, rows, kv=None):
+        dev = self.table.device
+        return F.KV4Batch(self.table, torch.tensor(kv or self.kv, dtype=torch.int32, device=dev),
+                          torch.tensor(np.cumsum([0] + list(rows)), dtype=torch.int32, device=dev), max(max(rows), 1))
+
+    def ws(self, op, rows, batch=None):
+        return F.alloc_workspace(F.fvattn_kv4_workspace_bytes(op, self.cache, batch or self.batch, rows, self.Hq),
+                                 self.table.device)
+
+    def append(self, rows, kv=None):
+        kv = kv or self.kv
+        b = self.batch_of(rows, kv)
+        cat = lambda x: torch.cat([t[n - r:n] for t, n, r in zip(x, kv, rows)]).cuda()
+        ws = self.ws(F.FVATTN_OP_KV4_APPEND, sum(rows), b)
+        F.fvattn_kv4_append(self.cache, b, cat(self.k), cat(self.v), ws)
+        assert F.fvattn_workspace_status(ws) == F.FVATTN_OK
+
+    def quantized(self, b):
+        """The oracle's codes and scales of sequence b's tokens: K codes, K scales, V codes, V scales."""
+        f = lambda x, s: O.quantize(x[b].float().numpy(), None if s is None else s.numpy())
+        return (*f(self.k, self.ks), *f(self.v, self.vs))
+
+    def values(self, b):
+        kc, ks, vc, vs = self.quantized(b)
+        h = lambda s: 1.0 if s is None else s.double().numpy()[:, None]
+        return O.dequantize(kc, ks) * h(self.ks), O.dequantize(vc, vs) * h(self.vs)
+
+    def records(self):
+        """The pool's records split: K codes [slots, H, block, d], K scales, V codes, V scales."""
+        p = self.cache.pages.cpu().numpy()
+        a, s = self.block * self.d // 2, self.block * self.d // 16
+        parts = [p[..., i:j] for i, j in ((0, a), (a, a + s), (a + s, 2 * a + s), (2 * a + s, 2 * a + 2 * s))]
+        out = []
+        for i, x in enumerate(parts):
+            x = x.reshape(*x.shape[:2], self.block, -1)
+            out.append(np.stack((x & 15, x >> 4), -1).reshape(*x.shape[:3], -1) if i % 2 == 0 else x)
+        return out
+
+    def make_q(self, dtype=None, spread=1.0, pad=0):
+        q = spread * torch.randn((self.rows + pad, self.Hq, self.d), generator=self.g)
+        return q.to(dtype or self.dtype)
+
+    def attend(self, q, causal=True, idx=None, cnt=None, scale=None, ws=None, stream=None):
+        qd = q if q.is_cuda else q.cuda()
+        out = torch.full(tuple(qd.shape), 77.0, dtype=qd.dtype, device=qd.device)
+        lse = torch.full(tuple(qd.shape[:2]), 77.0, device=qd.device)
+        ws = self.ws(F.FVATTN_OP_KV4_ATTN, qd.shape[0]) if ws is None else ws
+        F.fvattn_kv4_attn(self.cache, self.batch, qd, out, ws, scale=scale, causal=causal, lse=lse, kv_idx=idx,
+                          kv_cnt=cnt, stream=stream)
+        self.last_ws = ws
+        return out, lse
+
+    def check(self, q, out, lse, causal=True, lists=None, scale=None, rows=None):
+        """Every (row, head) (or the given rows) against the oracle, within the bound above."""
+        sc = float(np.float32(1 / math.sqrt(self.d) if scale is None else scale))
+        out, lse, qn = out.double().cpu().numpy(), lse.double().cpu().numpy(), q.double().cpu().numpy()
+        bf16 = q.dtype == BF16
+        half = 2.0 ** -8 if bf16 else 2.0 ** -24
+        G = self.Hq // self.H
+        r0 = 0
+        for b, (n, m) in enumerate(zip(self.kv, self.nrow)):
+            kv = self.values(b) if m else None
+            for i in range(m):
+                if rows is not None and r0 + i not in rows:
+                    continue
+                pos = n - m + i
+                keys = np.arange(max(0, min(n, pos + 1)) if causal else n)
+                for hq in range(self.Hq):
+                    h = hq // G
+                    kk = keys
+                    if lists is not None:
+                        kk = keys[np.isin(keys // self.block, lists[r0 + i][h])]
+                    k, v = kv[0][kk, h], kv[1][kk, h]
+                    ref, ref_lse, A, T = O.attend_row(qn[r0 + i, hq], k, v, sc)
+                    if len(kk) == 0:
+                        assert not out[r0 + i, hq].any() and lse[r0 + i, hq] == -np.inf
+                        continue
+                    S = abs(ref_lse) + T
+                    e_s = T * (self.d * 2.0 ** -24 + 2.0 ** -22) + S * 2.0 ** -22
+                    rel = 2 * e_s + 2.0 ** -21 + (2.0 ** -11 if bf16 else 2.0 ** -22)
+                    tol = (half + 2.0 ** -23) * np.abs(ref) + rel * A + len(kk) * 2.0 ** -29 * np.abs(v).max()
+                    err = np.abs(out[r0 + i, hq] - ref)
+                    assert np.all(err <= tol), (b, i, hq, float((err / tol).max()))
+                    assert abs(lse[r0 + i, hq] - ref_lse) <= 2 * e_s + 2.0 ** -20 + abs(ref_lse) * 2.0 ** -22, (b, i, hq)
+            r0 += m
+
+
+# ------------------------------------------------------------------ writing and reading back
+WRITE = [
+    # kv, H, d, block, scaled, dtype
+    ([1], 1, 64, 64, False, BF16),
+    ([128], 2, 128, 128, False, BF16),
+    ([130, 64, 1], 3, 128, 64, False, FP32),
+    ([300, 257, 0, 127], 2, 64, 128, True, BF16),
+    ([191], 5, 128, 64, True, FP32),
+]
+
+
+@pytest.mark.parametrize("kv,H,d,block,scaled,dtype", WRITE)
+def test_codes_scales_and_sums_are_exact(kv, H, d, block, scaled, dtype):
+    c = Case(kv, kv, H, d, block, seed=len(kv) + H, scaled=scaled, dtype=dtype, spread=1.3)
+    kc, ks, vc, vs = c.records()
+    ksum = c.cache.ksum.cpu().numpy()
+    for b, n in enumerate(kv):
+        want = c.quantized(b)
+        for t in range(n):
+            slot, at = c.table_np[b, t // block], t % block
+            for got, w in zip((kc, ks, vc, vs), want):
+                g, e = got[slot, :, at], w[t]
+                same = (g == e) | (((g & 7) == 0) & ((e & 7) == 0)) if got is kc or got is vc else g == e
+                assert np.all(same), (b, t)
+        plain = O.dequantize(want[0], want[1])
+        for pg in range(n // block):
+            for h in range(H):
+                s = O.page_sum(plain[pg * block:(pg + 1) * block, h])
+                assert np.array_equal(ksum[c.table_np[b, pg], h], s)
+    # what no row owns is as it was
+    owned = np.zeros((c.cache.num_pages, block), bool)
+    for b, n in enumerate(kv):
+        for t in range(n):
+            owned[c.table_np[b, t // block], t % block] = True
+    assert np.all(kc.transpose(0, 2, 1, 3)[~owned] == 7) and np.all(vs.transpose(0, 2, 1, 3)[~owned] == 0x77)
+
+
+@pytest.mark.parametrize("steps", [[1] * 9, [5, 64, 1, 60, 3], [127, 1, 2], [200]])
+def test_growing_by_steps_equals_one_write(steps):
+    n = sum(steps) + 70
+    a = Case([n, n], [n, n], 2, 64, 64, seed=3)
+    b = Case([n, n], [n, n], 2, 64, 64, seed=3, fill=False)
+    b.append([70, 70], kv=[70, 70])
+    at = 70
+    for s in steps:
+        at += s
+        b.append([s, s], kv=[at, at])
+    assert torch.equal(a.cache.pages, b.cache.pages)
+    full = [a.table_np[i, p] for i in range(2) for p in range(n // 64)]
+    assert torch.equal(a.cache.ksum[full], b.cache.ksum[full])
+
+
+def test_writing_a_position_again_replaces_it():
+    a, b = Case([130], [130], 2, 128, 64, seed=5), Case([130], [130], 2, 128, 64, seed=6)
+    b.k, b.v = a.k, a.v
+    b.append([100])                       # positions 30..129 with the other case's rows
+    b.append([130])
+    assert torch.equal(a.cache.pages[a.table_np[0, :3]], b.cache.pages[b.table_np[0, :3]])
+    assert torch.equal(a.cache.ksum[a.table_np[0, :2]], b.cache.ksum[b.table_np[0, :2]])
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_extreme_inputs(dtype):
+    c = Case([4], [4], 1, 64, 64, dtype=dtype, fill=False)
+    k = torch.zeros((4, 1, 64))
+    k[0, 0, 0], k[0, 0, 1] = 1e30, -5.0
+    k[1, 0, :16] = torch.linspace(-1, 1, 16) * 1e-4            # below half the smallest scale: all zero
+    k[1, 0, 16:32] = 0.02
+    k[2, 0, 0], k[2, 0, 1], k[2, 0, 2] = math.inf, -math.inf, 1.0
+    k[3, 0, 3] = -2688.0
+    c.k = c.v = [k.to(dtype)]
+    c.append([4])
+    out = [torch.empty((4, 1, 64), dtype=FP32, device="cuda") for _ in range(2)]
+    ws = c.ws(F.FVATTN_OP_KV4_READ, 4)
+    F.fvattn_kv4_read(c.cache, c.batch, *out, ws)
+    g = out[0].cpu()[:, 0]
+    assert g[0, 0] == 2688 and g[2, 0] == 2688 and g[2, 1] == -2688 and g[3, 3] == -2688
+    assert not g[1, :16].any() and torch.equal(out[0], out[1])
+    x = c.k[0].float().numpy()
+    x[2] = 0
+    want = O.dequantize(*O.quantize(x))
+    assert np.array_equal(g.numpy()[[0, 1, 3]], want[[0, 1, 3], 0])
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("d,block", [(64, 64), (128, 128), (128, 64)])
+def test_every_code_border(dtype, d, block):
+    """x on and one step beside every border t * s of two codes, for every scale significand."""
+    rows = []
+    for m in range(8, 16):
+        for e in (-6, 0, 7):
+            s = np.float32(m / 8 * 2.0 ** e)
+            for t in (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0):
+                x = torch.tensor(t * s, dtype=dtype)
+                lo, hi = (torch.nextafter(x, torch.tensor(v, dtype=dtype)) for v in (0.0, 1e9))
+                r = torch.zeros(16, dtype=dtype)
+                r[0] = float(6 * s)
+                r[1], r[2], r[3], r[4], r[5], r[6] = x, lo, hi, -x, -lo, -hi
+                rows.append(r)
+    x = torch.stack(rows)
+    x = torch.cat([x, torch.zeros((-len(x)) % (d // 16), 16, dtype=dtype)]).reshape(-1, 1, d)
+    c = Case([len(x)], [len(x)], 1, d, block, dtype=dtype, fill=False)
+    c.k = c.v = [x]
+    c.append([len(x)])
+    kc, ks, _, _ = c.records()
+    want, sc = O.quantize(x.float().numpy())
+    for t in range(len(x)):
+        slot = c.table_np[0, t // block]
+        g, w = kc[slot, 0, t % block], want[t, 0]
+        assert np.array_equal(ks[slot, 0, t % block], sc[t, 0])
+        assert np.all((g == w) | (((g & 7) == 0) & ((w & 7) == 0))), t
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("rows,pad", [([1, 1], 0), ([77, 3], 2), ([130, 200], 5)])
+def test_read_back(dtype, rows, pad):
+    c = Case([150, 200], rows, 3, 128, 64, seed=9, scaled=True)
+    c.nrow, rows = [min(a, b) for a, b in zip(rows, c.kv)], rows
+    b = c.batch_of(c.nrow)
+    n = sum(c.nrow)
+    out = [torch.full((n + pad, 3, 128), 55.0, dtype=dtype, device="cuda") for _ in range(2)]
+    ws = c.ws(F.FVATTN_OP_KV4_READ, n + pad, b)
+    F.fvattn_kv4_read(c.cache, b, *out, ws)
+    assert F.fvattn_workspace_status(ws) == F.FVATTN_OK
+    r = 0
+    for i, m in enumerate(c.nrow):
+        kc, ks, vc, vs = c.quantized(i)
+        for got, codes, scales, hs in ((out[0], kc, ks, c.ks), (out[1], vc, vs, c.vs)):
+            v = (O.dequantize(codes, scales).astype(np.float32) * hs.numpy()[:, None])[c.kv[i] - m:]
+            assert torch.equal(got[r:r + m].cpu(), torch.tensor(v).to(dtype))
+        r += m
+    assert torch.all(out[0][n:] == 55) and torch.all(out[1][n:] == 55)
+
+
+def test_append_takes_columns_of_a_fused_projection():
+    a = Case([90, 10], [90, 10], 2, 64, 64, seed=4)
+    b = Case([90, 10], [90, 10], 2, 64, 64, seed=4, fill=False)
+    k, v = torch.cat(b.k).cuda(), torch.cat(b.v).cuda()
+    fused = torch.randn((100, 8 * 64), device="cuda").to(BF16)
+    fused[:, 256:384], fused[:, 384:512] = k.flatten(1), v.flatten(1)
+    kk, vv = fused[:, 256:384].unflatten(1, (2, 64)), fused[:, 384:].unflatten(1, (2, 64))
+    F.fvattn_kv4_append(b.cache, b.batch, kk, vv, b.ws(F.FVATTN_OP_KV4_APPEND, 100))
+    assert torch.equal(a.cache.pages, b.cache.pages)
+
+
+def test_offsets_past_32_bits():
+    # 2^31 bytes of pool lie before the pages used: 117k records of 18,432 bytes and more
+    slots = (1 << 31) // 18432 + 40
+    cache = F.KV4Cache(slots, 1, 128, 128, "cuda")
+    n = 300
+    dev = cache.device
+    table = torch.tensor([[slots - 1, 3, slots - 7]], dtype=torch.int32, device=dev)
+    one = lambda *v: torch.tensor(v, dtype=torch.int32, device=dev)
+    batch = F.KV4Batch(table, one(n), one(0, n), n)
+    g = torch.Generator().manual_seed(1)
+    k, v = (torch.randn((n, 1, 128), generator=g).to(BF16) for _ in range(2))
+    ws = F.alloc_workspace(1 << 26, dev)
+    F.fvattn_kv4_append(cache, batch, k.cuda(), v.cuda(), ws)
+    ko, vo = torch.empty_like(k, device=dev), torch.empty_like(v, device=dev)
+    F.fvattn_kv4_read(cache, batch, ko, vo, ws)
+    want = O.dequantize(*O.quantize(k.float().numpy()))
+    assert np.array_equal(ko.float().cpu().numpy(), want)
+    q = torch.randn((n, 1, 128), generator=g).to(BF16)
+    out, lse = torch.empty_like(q, device=dev), torch.empty((n, 1), device=dev)
+    F.fvattn_kv4_attn(cache, batch, q.cuda(), out, ws, lse=lse)
+    ref, rl, _, _ = O.attend_row(q[-1, 0].double().numpy(), want[:, 0], O.dequantize(*O.quantize(v.float().numpy()))[:, 0],
+                                 128 ** -0.5)
+    assert abs(lse[-1, 0].item() - rl) < 1e-4 and np.abs(out[-1, 0].double().cpu().numpy() - ref).max() < 0.02
+
+
+# ------------------------------------------------------------------ choosing pages
+SELECT = [
+    # kv, rows, H, Hq, d, block, p, k_min, dtype, scaled
+    ([1], [1], 1, 1, 64, 64, 0.9, 1, BF16, False),
+    ([64], [1], 1, 2, 64, 64, 0.9, 1, BF16, False),
+    ([65], [1], 2, 2, 128, 64, 0.5, 1, FP32, False),
+    ([2000, 129, 700], [1, 1, 1], 2, 10, 128, 64, 0.9, 2, BF16, True),
+    ([1500, 900], [70, 3], 1, 3, 64, 128, 0.8, 1, BF16, False),
+    ([4500], [2], 1, 8, 64, 64, 0.95, 5, FP32, False),
+    ([1000, 0, 300], [5, 0, 2], 2, 2, 64, 64, 1.0, 1, BF16, False),
+    ([700], [4], 1, 64, 64, 64, 0.7, 3, BF16, False),
+    ([900], [3], 2, 4, 128, 64, 0.3, 100, BF16, True),
+]
+
+
+def _select(c, q, p, k_min, scale=None):
+    n = q.shape[0]
+    idx = torch.full((n, c.H, c.max_pages), -5, dtype=torch.int32, device="cuda")
+    cnt = torch.full((n, c.H), -5, dtype=torch.int32, device="cuda")
+    ws = c.ws(F.FVATTN_OP_KV4_SELECT, n)
+    F.fvattn_kv4_select(c.cache, c.batch, q.cuda(), p, k_min, idx, cnt, ws, scale=scale)
+    c.last_ws = ws
+    return idx, cnt
+
+
+def _want_lists(c, q, p, k_min, scale=None):
+    sc = float(np.float32(c.d ** -0.5 if scale is None else scale))
+    G = c.Hq // c.H
+    lists, qn = [], q.double().numpy()
+    r = 0
+    for b, (n, m) in enumerate(zip(c.kv, c.nrow)):
+        kc, ks, _, _ = c.quantized(b) if n else (None,) * 4
+        plain = O.dequantize(kc, ks) if n else None
+        for i in range(m):
+            o = (n - m + i) // c.block
+            per = []
+            for h in range(c.H):
+                sums = np.array([O.page_sum(plain[j * c.block:(j + 1) * c.block, h]) for j in range(o)]).reshape(o, c.d)
+                hs = 1.0 if c.ks is None else float(c.ks[h])
+                per.append(O.select_row(qn[r + i, h * G:(h + 1) * G], sums, c.block, sc * hs, float(np.float32(p)),
+                                        k_min))
+            lists.append(per)
+        r += m
+    return lists
+
+
+@pytest.mark.parametrize("kv,rows,H,Hq,d,block,p,k_min,dtype,scaled", SELECT)
+def test_lists_equal_the_oracles(kv, rows, H, Hq, d, block, p, k_min, dtype, scaled):
+    c = Case(kv, rows, H, d, block, seed=11, scaled=scaled, Hq=Hq)
+    q = c.make_q(dtype, spread=6.0, pad=2)          # sharp enough for short lists
+    idx, cnt = _select(c, q, p, k_min)
+    assert F.fvattn_workspace_status(c.last_ws) == F.FVATTN_OK
+    want = _want_lists(c, q, p, k_min)
+    idx, cnt = idx.cpu().numpy(), cnt.cpu().numpy()
+    for r, per in enumerate(want):
+        for h, w in enumerate(per):
+            assert cnt[r, h] == len(w) and list(idx[r, h, :len(w)]) == w, (r, h)
+            assert np.all(idx[r, h, len(w):] == -5)
+    assert np.all(cnt[c.rows:] == -5) and np.all(idx[c.rows:] == -5)
+
+
+def test_tied_pages_go_to_the_lower_index():
+    c = Case([64 * 9 + 1], [1], 1, 64, 64, seed=2, Hq=3, fill=False)
+    page = torch.randn((64, 1, 64), generator=c.g).to(BF16)
+    c.k = [torch.cat([page] * 9 + [page[:1]])]
+    c.append(c.kv)
+    idx, cnt = _select(c, c.make_q(), 0.5, 1)
+    assert idx[0, 0, :cnt[0, 0]].tolist() == [0, 1, 2, 3, 4, 9]
+    idx, cnt = _select(c, c.make_q(), 0.01, 3)
+    assert idx[0, 0, :cnt[0, 0]].tolist() == [0, 1, 2, 9]
+
+
+def test_select_takes_columns_of_a_fused_projection():
+    c = Case([700, 300], [3, 2], 2, 64, 64, seed=8, Hq=4)
+    q = c.make_q(spread=5.0)
+    wide = torch.randn((5, 6 * 64), device="cuda").to(BF16)
+    wide[:, 64:320] = q.flatten(1).cuda()
+    a = _select(c, q, 0.8, 2)
+    b = _select(c, wide[:, 64:320].unflatten(1, (4, 64)), 0.8, 2)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+# ------------------------------------------------------------------ attention
+ATTEND = [
+    # kv, rows, H, Hq, d, block, dtype, causal, scaled
+    ([1], [1], 1, 1, 64, 64, BF16, True, False),
+    ([1, 2, 63, 64, 65], [1] * 5, 2, 2, 128, 64, BF16, True, False),
+    ([127, 128, 129, 700], [1] * 4, 1, 8, 128, 128, BF16, True, True),
+    ([1000], [1], 3, 15, 128, 64, BF16, True, False),
+    ([513, 40], [1, 1], 1, 16, 64, 128, BF16, True, False),
+    ([400], [1], 1, 40, 64, 64, BF16, True, False),
+    ([300], [1], 1, 64, 128, 128, BF16, True, False),
+    ([700, 90], [5, 3], 2, 6, 64, 64, FP32, True, True),
+    ([260], [1], 2, 4, 128, 128, FP32, True, False),
+    ([130, 0, 77], [9, 0, 1], 2, 4, 128, 64, BF16, True, False),
+    ([200, 100], [33, 100], 1, 4, 128, 128, BF16, True, False),
+    ([333, 257], [333, 130], 2, 2, 64, 128, BF16, True, True),
+    ([300], [150], 1, 3, 128, 64, BF16, False, False),
+    ([513], [300], 1, 1, 128, 128, BF16, False, False),
+    ([150], [40], 1, 3, 128, 128, FP32, False, False),
+    ([300], [140], 2, 2, 64, 64, BF16, False, True),
+]
+
+
+@pytest.mark.parametrize("kv,rows,H,Hq,d,block,dtype,causal,scaled", ATTEND)
+def test_attention(kv, rows, H, Hq, d, block, dtype, causal, scaled):
+    c = Case(kv, rows, H, d, block, seed=sum(kv), scaled=scaled, Hq=Hq)
+    q = c.make_q(dtype, spread=2.0, pad=3)
+    out, lse = c.attend(q, causal)
+    assert F.fvattn_workspace_status(c.last_ws) == F.FVATTN_OK
+    assert torch.all(out[c.rows:] == 77) and torch.all(lse[c.rows:] == 77)     # rows of no sequence
+    some = None if c.rows <= 60 else set(range(0, c.rows, 7)) | {c.rows - 1}
+    c.check(q, out, lse, causal, rows=some)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("causal", [True, False])
+def test_rows_that_see_nothing(dtype, causal):
+    # more rows than tokens: the first ones stand before the sequence; an empty sequence has nothing to see
+    c = Case([3, 0, 70], [5, 2, 1], 1, 64, 64, seed=7, Hq=4, dtype=dtype, fill=False)
+    c.append([3, 0, 70])
+    q = c.make_q()
+    out, lse = c.attend(q, causal)
+    assert F.fvattn_workspace_status(c.last_ws) == F.FVATTN_OK
+    c.check(q, out, lse, causal)
+    dead = [0, 1, 5, 6] if causal else [5, 6]
+    assert not out[dead].any() and torch.all(lse[dead] == -math.inf)
+
+
+@pytest.mark.parametrize("rows", [[1, 1], [40, 150]])
+@pytest.mark.parametrize("spread", [1e-6, 30.0, 1e4])
+def test_blunt_and_sharp_logits(rows, spread):
+    c = Case([900, 333], rows, 1, 128, 128, seed=13, Hq=4)
+    q = c.make_q(spread=spread)
+    scale = 0.01 if spread > 100 else None
+    out, lse = c.attend(q, scale=scale)
+    c.check(q, out, lse, scale=scale, rows=set(range(0, c.rows, 11)) | {0, c.rows - 1})
+
+
+@pytest.mark.parametrize("rows", [[1], [70]])
+def test_growing_logits(rows):
+    """Keys that point ever more along q: the running maximum rises at every page."""
+    c = Case([1100], rows, 1, 64, 64, seed=14, Hq=1, fill=False)
+    direction = torch.randn(64, generator=c.g)
+    ramp = torch.linspace(-3, 3, 1100)[:, None, None]
+    c.k = [(ramp * direction + 0.1 * torch.randn((1100, 1, 64), generator=c.g)).to(BF16)]
+    c.append(c.kv)
+    q = (5 * direction).to(BF16).expand(c.rows, 1, 64).contiguous()
+    out, lse = c.attend(q)
+    c.check(q, out, lse, rows=set(range(0, c.rows, 9)))
+
+
+@pytest.mark.parametrize("big", [1e30, 1e-30])
+@pytest.mark.parametrize("rows", [[2], [200]])
+def test_range_of_q(big, rows):
+    c = Case([260], rows, 1, 64, 64, seed=15, Hq=2)
+    q = c.make_q()
+    ref, rl = c.attend(q, scale=0.125)
+    got, gl = c.attend((q.float() * 2.0 ** round(math.log2(big))).to(BF16), scale=0.125 * 2.0 ** -round(math.log2(big)))
+    assert torch.equal(ref, got) and torch.equal(rl, gl)
+
+
+@pytest.mark.parametrize("rows,G", [([1, 1], 1), ([1, 1], 5), ([3, 2], 8), ([2, 1], 20)])
+@pytest.mark.parametrize("block,dtype", [(64, BF16), (128, BF16), (64, FP32)])
+def test_attention_over_selected_pages(rows, G, block, dtype):
+    c = Case([1400, 650], rows, 2, 64, block, seed=16, Hq=2 * G)
+    q = c.make_q(dtype, spread=4.0)
+    idx, cnt = _select(c, q, 0.7, 2)
+    lists = [[idx[r, h, :cnt[r, h]].tolist() for h in range(2)] for r in range(c.rows)]
+    for causal in (True, False):
+        out, lse = c.attend(q, causal, idx, cnt)
+        assert F.fvattn_workspace_status(c.last_ws) == F.FVATTN_OK
+        c.check(q, out, lse, causal, lists=lists)
+
+
+def test_lists_of_every_page_equal_no_lists():
+    c = Case([900, 500], [2, 3], 2, 128, 64, seed=17, Hq=8)
+    q = c.make_q()
+    idx = torch.arange(c.max_pages, dtype=torch.int32, device="cuda").expand(5, 2, -1).contiguous()
+    cnt = torch.tensor([15] * 2 + [8] * 3, dtype=torch.int32, device="cuda")[:, None].expand(5, 2).contiguous()
+    a, la = c.attend(q, True, idx, cnt)
+    b, lb = c.attend(q, True)
+    assert (a.float() - b.float()).abs().max() <= 2.0 ** -7 * b.float().abs().max()
+    assert (la - lb).abs().max() < 1e-4
+
+
+def test_bad_lists_are_left_out_and_recorded():
+    c = Case([900], [3], 1, 64, 64, seed=18, Hq=2)          # pages 0..14
+    q = c.make_q()
+    idx = torch.zeros((3, 1, c.max_pages), dtype=torch.int32, device="cuda")
+    cnt = torch.tensor([[6], [2], [1]], dtype=torch.int32, device="cuda")
+    idx[0, 0, :6] = torch.tensor([2, 2, 1, 5, 99, 14], dtype=torch.int32)      # repeated, descending, out of range
+    idx[1, 0, :2] = torch.tensor([-3, 4], dtype=torch.int32)
+    out, lse = c.attend(q, True, idx, cnt)
+    assert F.fvattn_workspace_status(c.last_ws) == F.FVATTN_ERR_INVALID_ARG
+    # each entry has to be above the one before it, whatever became of that one: 14 is not
+    c.check(q, out, lse, True, lists=[[[2, 5]], [[4]], [[0]]])
+    cnt[1] = 0
+    idx[0, 0, :6] = torch.tensor([0, 1, 2, 5, 9, 14], dtype=torch.int32)
+    out, lse = c.attend(q, True, idx, cnt)
+    assert F.fvattn_workspace_status(c.last_ws) == F.FVATTN_OK
+    assert not out[1].any() and torch.all(lse[1] == -math.inf)
+
+
+@pytest.mark.parametrize("rows", [[1, 1], [60, 100]])
+def test_bad_tables_and_lengths_are_recorded(rows):
+    c = Case([300, 500], rows, 1, 64, 64, seed=19, Hq=2)
+    q = c.make_q()
+    good, gl = c.attend(q)
+    first = rows[0]
+    table = c.table.clone()
+    c.batch.table[0, 1] = c.cache.num_pages + 5             # sequence 0 loses a page; sequence 1 keeps its result
+    out, lse = c.attend(q)
+    assert F.fvattn_workspace_status(c.last_ws) == F.FVATTN_ERR_INVALID_ARG
+    assert torch.equal(out[first:], good[first:]) and torch.isfinite(out).all()
+    idx, cnt = _select(c, q, 0.9, 1)
+    assert F.fvattn_workspace_status(c.last_ws) == F.FVATTN_ERR_INVALID_ARG
+    c.batch.table.copy_(table)
+    c.batch.kv_len[0] = (c.max_pages + 1) * 64              # longer than its table row
+    c.batch.table.clamp_(min=0)
+    out, lse = c.attend(q)
+    assert F.fvattn_workspace_status(c.last_ws) == F.FVATTN_ERR_INVALID_ARG
+    assert torch.equal(out[first:], good[first:])
+    c.batch.kv_len[0] = -4
+    out, lse = c.attend(q)
+    assert F.fvattn_workspace_status(c.last_ws) == F.FVATTN_ERR_INVALID_ARG
+    assert not out[:first].any() and torch.equal(out[first:], good[first:])
+
+
+def test_writes_outside_the_table_are_refused_on_the_device():
+    c = Case([100, 100], [100, 100], 1, 64, 64, seed=20)
+    before = c.cache.pages.clone()
+    k = torch.randn((8, 1, 64), device="cuda").to(BF16)
+    ws = c.ws(F.FVATTN_OP_KV4_APPEND, 8)
+    for kv, cu in (([2, 100], [0, 8, 8]), ([5000, 100], [0, 4, 4]), ([-3, 100], [0, 8, 8])):
+        b = F.KV4Batch(c.table, torch.tensor(kv, dtype=torch.int32, device="cuda"),
+                       torch.tensor(cu, dtype=torch.int32, device="cuda"), 8)
+        F.fvattn_kv4_append(c.cache, b, k, k, ws)
+        assert F.fvattn_workspace_status(ws) == F.FVATTN_ERR_INVALID_ARG
+    slot = int(c.table_np[0, 0])
+    keep = [s for s in range(c.cache.num_pages) if s not in c.table_np[0]]
+    assert torch.equal(c.cache.pages[keep], before[keep])
+    # the two valid positions of the first call were written, nothing behind them
+    assert not torch.equal(c.cache.pages[slot], before[slot])
+    b = F.KV4Batch(c.table, torch.tensor([2, 100], dtype=torch.int32, device="cuda"),
+                   torch.tensor([0, 8, 8], dtype=torch.int32, device="cuda"), 8)
+    ko, vo = (torch.full((8, 1, 64), 3.0, device="cuda") for _ in range(2))
+    F.fvattn_kv4_read(c.cache, b, ko, vo, ws)
+    assert F.fvattn_workspace_status(ws) == F.FVATTN_ERR_INVALID_ARG
+    assert not ko[:6].any() and ko[6:].abs().sum() > 0
+
+
+# ------------------------------------------------------------------ together, streams, graphs, refusals
+def _path_inputs(c, rows, seed):
+    g = torch.Generator().manual_seed(seed)
+    mk = lambda H: torch.randn((rows, H, c.d), generator=g).to(BF16)
+    return mk(c.Hq), mk(c.H), mk(c.H)
+
+
+@pytest.mark.parametrize("p", [None, 0.8])
+def test_path_grows_sequences(p):
+    """A prompt, then single tokens: every step writes, chooses and attends; the last step's outputs and lists
+    against the oracle on everything written."""
+    kv, H, Hq, d, block = [150, 201], 2, 6, 64, 64
+    c = Case(kv, kv, H, d, block, seed=21, Hq=Hq, fill=False)
+    path = F.KV4Path(c.cache, Hq, sum(kv), 2, c.max_pages, BF16, p=p, k_min=1)
+    q0 = [torch.randn((n, Hq, d), generator=c.g).mul(4).to(BF16) for n in kv]
+    at = [n - 6 for n in kv]
+    take = lambda x, lo, hi: torch.cat([t[a:b] for t, a, b in zip(x, lo, hi)]).cuda()
+    path(c.batch_of(at, at), take(q0, [0, 0], at), take(c.k, [0, 0], at), take(c.v, [0, 0], at))
+    for _ in range(6):
+        nxt = [a + 1 for a in at]
+        out = path(c.batch_of([1, 1], nxt), take(q0, at, nxt), take(c.k, at, nxt), take(c.v, at, nxt))
+        at = nxt
+    for ws in (path.ws_append, path.ws_attn) + (() if p is None else (path.ws_select,)):
+        assert F.fvattn_workspace_status(ws) == F.FVATTN_OK
+    c.nrow, c.rows = [1, 1], 2
+    q = take(q0, [n - 1 for n in kv], kv)
+    lists = None if p is None else _want_lists(c, q.cpu(), p, 1)
+    c.check(q, out, path.lse[:2], lists=lists)
+
+
+def test_captured_step_follows_the_lengths():
+    """One captured step replayed while the lengths, the rows and the inputs change on the device."""
+    c = Case([140, 90], [1, 1], 2, 128, 64, seed=22, Hq=8)
+    path = F.KV4Path(c.cache, 8, 2, 2, c.max_pages, BF16, p=0.9, k_min=1)
+    batch = c.batch_of([1, 1], [100, 50])
+    q, k, v = (t.cuda() for t in _path_inputs(c, 2, 1))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        path(batch, q, k, v)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = path(batch, q, k, v)
+    other = F.KV4Path(c.cache, 8, 2, 2, c.max_pages, BF16, p=0.9, k_min=1)
+    for step, kv in enumerate(([101, 51], [129, 64], [140, 90])):
+        batch.kv_len.copy_(torch.tensor(kv, dtype=torch.int32))
+        for t, s in zip((q, k, v), _path_inputs(c, 2, 10 + step)):
+            t.copy_(s)
+        graph.replay()
+        got = out.clone()
+        want = other(c.batch_of([1, 1], kv), q, k, v)
+        assert torch.equal(got, want), kv
+
+
+def test_two_calls_at_once_and_repeats_are_bit_identical():
+    c = Case([3000, 1700], [1, 1], 2, 128, 64, seed=23, Hq=8)
+    d = Case([700, 900], [100, 130], 1, 64, 128, seed=24, Hq=4)
+    qc, qd = c.make_q().cuda(), d.make_q().cuda()
+    want_c, want_d = c.attend(qc), d.attend(qd)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    wc, wd = c.ws(F.FVATTN_OP_KV4_ATTN, 2), d.ws(F.FVATTN_OP_KV4_ATTN, 230)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(s1):
+            got_c = c.attend(qc, ws=wc)
+        with torch.cuda.stream(s2):
+            got_d = d.attend(qd, ws=wd)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got_c + got_d, want_c + want_d))
+
+
+def test_an_explicit_stream_is_used():
+    c = Case([500], [1], 1, 64, 64, seed=25, Hq=4)
+    q = c.make_q().cuda()
+    want, _ = c.attend(q)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got, _ = c.attend(q, stream=s)
+    s.synchronize()
+    # the buffers were filled on the current stream before: wait for both
+    torch.cuda.synchronize()
+    assert got.shape == want.shape
+
+
+def test_no_rows():
+    c = Case([100], [1], 1, 64, 64, seed=26)
+    e = torch.empty((0, 1, 64), dtype=BF16, device="cuda")
+    b = F.KV4Batch(c.table, c.batch.kv_len, torch.zeros(2, dtype=torch.int32, device="cuda"), 1)
+    before = c.cache.pages.clone()
+    ws = c.ws(F.FVATTN_OP_KV4_ATTN, 0)
+    F.fvattn_kv4_append(c.cache, b, e, e, ws)
+    F.fvattn_kv4_read(c.cache, b, e, e.clone(), ws)
+    F.fvattn_kv4_attn(c.cache, b, e, e.clone(), ws)
+    assert torch.equal(before, c.cache.pages)
+
+
+def test_the_binding_refuses():
+    c = Case([100, 60], [2, 1], 2, 64, 64, seed=27, Hq=4)
+    ws = F.alloc_workspace(1 << 20, "cuda")
+    q = c.make_q().cuda()
+    out = torch.empty_like(q)
+    k = torch.zeros((3, 2, 64), dtype=BF16, device="cuda")
+    att = lambda **kw: F.fvattn_kv4_attn(**{**dict(cache=c.cache, batch=c.batch, q=q, out=out, workspace=ws), **kw})
+    for bad in (dict(out=out.float()), dict(out=out[:2]), dict(q=q.cpu()), dict(q=q.transpose(0, 1)),
+                dict(lse=torch.empty((3, 2), device="cuda")), dict(kv_idx=torch.zeros(3, dtype=torch.int32).cuda()),
+                dict(workspace=ws.cpu())):
+        with pytest.raises((ValueError, TypeError)):
+            att(**bad)
+    with pytest.raises(F.FVAttnError):
+        att(q=q[:, :3].contiguous(), out=out[:, :3].contiguous())     # 3 query heads for 2 KV heads
+    with pytest.raises(F.FVAttnError):
+        att(out=q)
+    with pytest.raises(F.FVAttnError):
+        att(scale=-1.0)
+    app = lambda **kw: F.fvattn_kv4_append(**{**dict(cache=c.cache, batch=c.batch, k=k, v=k, workspace=ws), **kw})
+    for bad in (dict(v=k.float()), dict(k=k[:2]), dict(k=k.half(), v=k.half()), dict(k=k[..., :32]),
+                dict(k=torch.zeros((3, 2 * 64 + 4), dtype=BF16, device="cuda")[:, :128].unflatten(1, (2, 64)))):
+        with pytest.raises((ValueError, TypeError)):
+            app(**bad)
+    with pytest.raises(ValueError):
+        F.KV4Batch(c.table, c.batch.kv_len[:1], c.batch.cu, 1)
+    with pytest.raises(ValueError):
+        F.KV4Batch(c.table, c.batch.kv_len, c.batch.cu, 0)
+    with pytest.raises(TypeError):
+        F.KV4Batch(c.table.long(), c.batch.kv_len, c.batch.cu, 1)
+    with pytest.raises(ValueError):
+        F.KV4Cache(4, 2, 96, 64)
