@@ -1,6 +1,7 @@
 // kv4_api.cu -- the extern "C" entry points of the paged 4-bit key/value cache
 // (declared in include/fvattn.h): host-side validation, workspace layout, dispatch.
 // No entry point allocates device memory or synchronizes the host.
+#include <atomic>
 #include <cmath>
 
 #include "kv4.cuh"
@@ -15,8 +16,10 @@ cudaError_t launch_select(const Cache& c, const Batch& bt, const void* q, long l
                           float scale, float p, int k_min, int d, int block, int* kv_idx, int* kv_cnt,
                           int* status, cudaStream_t st);
 cudaError_t launch_attn(const Cache& c, const Batch& bt, const void* q, long long q_stride, int Hq, void* out,
-                        float* lse, bool bf16, float scale, int causal, int d, int block, const int* kv_idx,
-                        const int* kv_cnt, int* status, cudaStream_t st);
+                        float* lse, bool bf16, float scale, int causal, int d, int block, int max_q, const int* kv_idx,
+                        const int* kv_cnt, int* status, uint8_t* ws, int num_sms, cudaStream_t st);
+size_t attn_ws_bytes(int d);
+size_t attn_ws_clear();
 }  // namespace kv4
 }  // namespace fvattn
 
@@ -44,6 +47,7 @@ bool valid_sizes(const fvattn_kv4_cache* c, const fvattn_kv4_batch* b) {
   if ((c->d != 64 && c->d != 128) || (c->block != 64 && c->block != 128)) return false;
   if (b->B < 1 || b->B > kMaxBatch || b->max_pages < 1 || b->rows < 0 || b->rows > kMaxRows || b->max_q < 1)
     return false;
+  if (static_cast<long long>(b->rows) * c->H > 0x3FFFFFFFll) return false;   // (row, KV head) pairs are ints
   return static_cast<long long>(b->max_pages) * c->block <= kMaxTokens;
 }
 
@@ -78,10 +82,26 @@ size_t pool_bytes(const fvattn_kv4_cache* c) {
   return static_cast<size_t>(c->num_pages) * c->H * c->block * (c->d + c->d / 8);
 }
 
-// Workspace check, and the status word cleared on the stream.
-fvattn_status begin(void* ws, size_t have, size_t need, cudaStream_t st) {
+// Workspace check, and the header (and `clear` bytes behind it) cleared on the stream.
+fvattn_status begin(void* ws, size_t have, size_t need, cudaStream_t st, size_t clear = 0) {
   if (!ws || !aligned(ws, 256) || have < need) return FVATTN_ERR_WORKSPACE;
-  return cudaMemsetAsync(ws, 0, kWsHeaderBytes, st) == cudaSuccess ? FVATTN_OK : FVATTN_ERR_CUDA;
+  return cudaMemsetAsync(ws, 0, kWsHeaderBytes + clear, st) == cudaSuccess ? FVATTN_OK : FVATTN_ERR_CUDA;
+}
+
+// SM count of the current device, kept after the first look-up (every writer of an entry stores
+// the same value, so calls from several host threads may race to fill it).
+int device_sm_count() {
+  static std::atomic<int> cache[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev >= 0 && dev < 64) {
+    const int n = cache[dev].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+  }
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev >= 0 && dev < 64) cache[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 fvattn_status from_cuda(cudaError_t e) { return e == cudaSuccess ? FVATTN_OK : FVATTN_ERR_CUDA; }
@@ -98,7 +118,8 @@ size_t fvattn_kv4_workspace_bytes(fvattn_op op, const fvattn_kv4_cache* cache, c
     case FVATTN_OP_KV4_READ: return kWsHeaderBytes;
     case FVATTN_OP_KV4_SELECT:
       return valid_heads(cache, Hq) && batch->max_pages <= kMaxSelectPages ? kWsHeaderBytes : 0;
-    case FVATTN_OP_KV4_ATTN: return valid_heads(cache, Hq) ? kWsHeaderBytes : 0;
+    case FVATTN_OP_KV4_ATTN:
+      return valid_heads(cache, Hq) ? kWsHeaderBytes + fvattn::align_up(fvattn::kv4::attn_ws_bytes(cache->d), 256) : 0;
     default: return 0;
   }
 }
@@ -185,12 +206,15 @@ fvattn_status fvattn_kv4_attn(const fvattn_kv4_cache* cache, const fvattn_kv4_ba
   if (!ok || overlap(q, nq, out, static_cast<size_t>(batch->rows) * Hq * cache->d * es)) return FVATTN_ERR_INVALID_ARG;
   const size_t need = fvattn_kv4_workspace_bytes(FVATTN_OP_KV4_ATTN, cache, batch, Hq);
   auto st = static_cast<cudaStream_t>(stream);
-  const fvattn_status s = begin(workspace, workspace_bytes, need, st);
+  const fvattn_status s = begin(workspace, workspace_bytes, need, st, fvattn::kv4::attn_ws_clear());
   if (s != FVATTN_OK || batch->rows == 0) return s;
+  const int sms = device_sm_count();
+  if (sms <= 0) return FVATTN_ERR_CUDA;
   auto hdr = static_cast<fvattn::WsHeader*>(workspace);
   return from_cuda(fvattn::kv4::launch_attn(cache_of(cache), batch_of(batch), q, q_stride, Hq, out, lse,
                                             dtype == FVATTN_BF16, scale, causal != 0, cache->d, cache->block,
-                                            kv_idx, kv_cnt, &hdr->status, st));
+                                            batch->max_q, kv_idx, kv_cnt, &hdr->status,
+                                            static_cast<uint8_t*>(workspace) + kWsHeaderBytes, sms, st));
 }
 
 }  // extern "C"

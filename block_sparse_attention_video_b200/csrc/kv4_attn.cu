@@ -1,107 +1,813 @@
-// kv4_attn.cu -- attention over the 4-bit cache: one warp per (row, query head), one
-// pass over the visible keys with the running maximum and sum of the softmax, fp32.
+// kv4_attn.cu -- attention of few query rows over the 4-bit cache: single tokens,
+// drafts, selected pages, and every fp32 call. One pass over the cache with the running
+// maximum and sum of the softmax, split over the pages and joined in a fixed order.
+//
+// Unit: up to RT = 8 NT query rows (a sequence's (row, query head) pairs that share a KV
+// head, in that order; with lists, the query heads of one row) against the pages they
+// see. A step is 128 keys: one page of 128 tokens or two of 64. The steps of all units
+// form one line that is cut into equal pieces, one per block, so ragged lengths balance
+// by themselves: every block adds up the units' lengths and finds its piece. A unit that
+// lies in several pieces leaves partial sums in the workspace; the block that arrives
+// last joins them in the order of the pieces, so the result does not depend on who that
+// is.
+//
+// A block is one producer warp, which brings whole page records into a ring of shared
+// memory (one bulk copy a page, 18 KB at d 128), and eight consumer warps with 16 keys of
+// the step each. What bounds it is HBM: d + d/8 bytes of K and V a token and KV head.
+//
+// Arithmetic per warp and step, on m16n8k16 fp16 products with fp32 sums:
+//   S^T [16 keys x 8 rows]     = K [16 x d] Q^T      K's codes become fp16 in registers
+//   O^T [16 channels x 8 rows] += V^T [16 x 16 keys] P^T
+// The transposed forms put keys (channels) on the 16-wide side and the few query rows on
+// the 8-wide one. Both operands come out of shared memory as 4-bit codes and are expanded
+// in registers; E2M1 times E4M3 needs at most 6 significant bits, so the fp16 operands
+// hold the stored values exactly. The order of channels inside a dot product and of keys
+// inside a sum is free, and is chosen so that a lane reads whole 16-byte (K) and 8-byte
+// (V) words of the plain record: k-slot j of lane t is channel (HD/4) t + 4 j.., row g of
+// V's tile i is channel (HD/8) g + 2 i. P^T's registers are S^T's transposed
+// (movmatrix).
+//
+// Q is scaled by a power of two per row so that its largest element lies in [2^13, 2^14)
+// (undone in the logits), so bf16 enters exactly. fp32 Q and P are split into two fp16
+// parts, and O is then summed outside the tensor core, whose sums are cut off and not
+// rounded.
+#include <cfloat>
+
 #include "kv4.cuh"
+#include "sm100.cuh"
 
 namespace fvattn {
 namespace kv4 {
 
-template <typename T, int HD>
-__global__ void __launch_bounds__(128)
-    attn_kernel(const Cache c, const Batch bt, const T* __restrict__ q, long long q_stride, int Hq,
-                T* __restrict__ out, float* __restrict__ lse, float scale, int causal, int block,
-                const int* __restrict__ kv_idx, const int* __restrict__ kv_cnt, int* status) {
-  constexpr int C = HD / 32;   // channels per lane
-  const long long unit = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (unit == 0 && lane == 0 && __ldg(bt.cu + bt.B) > bt.rows) record_status(status, FVATTN_ERR_INVALID_ARG);
-  const int r = static_cast<int>(unit / Hq);
-  const int hq = static_cast<int>(unit - static_cast<long long>(r) * Hq);
-  if (r >= bt.rows) return;
-  int b;
-  if (!sequence_of(bt, r, b)) return;
-  const int h = hq / (Hq / c.H);
-  const int n = held(bt, b, block, status);
-  const int pos = n - (__ldg(bt.cu + b + 1) - r);
-  const int seen = causal ? min(max(pos + 1, 0), n) : n;
-  const Layout L(HD, block);
-  const float ks = scale * (c.k_scale ? __ldg(c.k_scale + h) : 1.f);
-  float qv[C], o[C], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < C; ++i) {
-    qv[i] = static_cast<float>(q[static_cast<long long>(r) * q_stride + hq * HD + lane * C + i]) * ks;
-    o[i] = 0.f;
+constexpr int kConsumers = 8;                       // consumer warps, 16 keys each
+constexpr int kThreads = (kConsumers + 1) * 32;
+constexpr int kStep = kConsumers * 16;              // keys per step
+constexpr float kFloor = -3.0e38f;                  // running max before any key
+constexpr float kRaise = 8.f;                       // the max is raised when exceeded by 2^8
+constexpr float kHead = 6.f;                        // P <= 2^(6 + 8) stays inside fp16
+constexpr float kLn2 = 0.69314718055994531f;
+
+struct AttnParams {
+  Cache c;
+  Batch bt;
+  const void* q;
+  long long q_stride;
+  void* out;
+  float* lse;
+  const int* kv_idx;      // nullptr: every page
+  const int* kv_cnt;
+  float scale_log2;       // scale * log2(e)
+  int G, causal, block;
+  int* status;
+  int* arrived;           // [gridDim] blocks that left their part of the unit begun there
+  float* part;            // [gridDim][2] partial sums: O [RT][HD], max [RT], sum [RT]
+};
+
+// A unit and the piece of it that a step belongs to, published with each stage.
+struct Meta {
+  int key0[2];            // first key of the stage's pages; -1: no such page
+  int first, last;        // first / last step of the unit in this block
+  int cu, q, n;           // the sequence: first row, rows, tokens held
+  int m0, mc;             // first (row, head) pair and their number
+  int h;                  // KV head
+  int seen;               // keys that the unit's last row sees
+  int begin, end;         // blocks that hold the unit's first and last step
+  int pad[3];
+};
+static_assert(sizeof(Meta) == 64, "sixteen words, written by sixteen lanes");
+
+template <int HD, int NT>
+struct Shape {
+  static constexpr int RT = 8 * NT;
+  static constexpr int kStageBytes = kStep * (HD + HD / 8);
+  // about 92 KB of ring a block with two blocks on an SM (NT 1), 184 KB with one
+  static constexpr int kStages = (NT == 1 ? 5 : 10) * (128 / HD);
+  static constexpr int kPart = RT * HD + 2 * RT;    // floats of a partial result
+};
+
+template <int HD, int NT>
+struct __align__(128) AttnSmem {
+  using S = Shape<HD, NT>;
+  uint8_t ring[S::kStages][S::kStageBytes];
+  float slab[4][S::RT][HD];
+  float mx[2][kConsumers][S::RT];
+  float sum[2][kConsumers][S::RT];
+  Meta meta[S::kStages];
+  uint64_t full[S::kStages];
+  uint64_t empty[S::kStages];
+  uint64_t sync;
+  long long warp_total[kThreads / 32];
+  long long lo, hi, rem, total;
+  int entry, blocks;
+  int joiner;
+  int abort_flag;
+};
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 8x8 matrix of 16-bit elements, one 32-bit row piece a lane, transposed across the warp.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint32_t x) { return __half22float2(*reinterpret_cast<__half2*>(&x)); }
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t two_codes) {
+  const __half2 h = e4m3x2_to_half2(two_codes);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(float x) { return x; }
+
+// Entries are what the units are counted by: without lists, tiles of RT pairs of a
+// sequence (each counts for all KV heads); with lists, (row, KV head) (each counts for
+// all tiles of its query heads). Tiles are numbered without a prefix sum: sequence b owns
+// those from cu[b] G / RT + b on, room for the at most ceil(q G / RT) it needs.
+template <int RT>
+struct Entries {
+  const AttnParams& P;
+  __device__ long long count() const {
+    return P.kv_idx ? static_cast<long long>(P.bt.rows) * P.c.H
+                    : static_cast<long long>(P.bt.rows) * P.G / RT + P.bt.B;
   }
-  const int pages = (seen + block - 1) / block;
-  const int* list = kv_idx ? kv_idx + (static_cast<size_t>(r) * c.H + h) * bt.max_pages : nullptr;
-  int cnt = pages, held_pages = (n + block - 1) / block, before = -1;
-  if (list) {
-    cnt = __ldg(kv_cnt + static_cast<size_t>(r) * c.H + h);
-    if (cnt < 0 || cnt > bt.max_pages) {
-      if (lane == 0) record_status(status, FVATTN_ERR_INVALID_ARG);
-      cnt = min(max(cnt, 0), bt.max_pages);
+  __device__ int times() const { return P.kv_idx ? (P.G + RT - 1) / RT : P.c.H; }
+  // Steps of a unit of entry e and where it lies; 0 if the entry is not in use.
+  __device__ int steps(long long e, int& b, int& m0, int& seen, Meta* m) const {
+    const Batch& bt = P.bt;
+    if (P.kv_idx) {
+      const int r = static_cast<int>(e / P.c.H);
+      if (!sequence_of(bt, r, b)) return 0;
+      int cnt = __ldg(P.kv_cnt + e);
+      if (cnt < 0 || cnt > bt.max_pages) {
+        record_status(P.status, FVATTN_ERR_INVALID_ARG);
+        cnt = min(max(cnt, 0), bt.max_pages);
+      }
+      m0 = (r - __ldg(bt.cu + b)) * P.G;
+      if (m) {
+        m->cu = __ldg(bt.cu + b);
+        m->q = __ldg(bt.cu + b + 1) - m->cu;
+        m->n = held(bt, b, P.block, P.status);
+        const int pos = m->n - m->q + (r - m->cu);
+        seen = P.causal ? min(max(pos + 1, 0), m->n) : m->n;
+      }
+      return max(1, (cnt * P.block + kStep - 1) / kStep);
+    }
+    int lo = 0, hi = bt.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (static_cast<long long>(__ldg(bt.cu + mid)) * P.G / RT + mid <= e) lo = mid; else hi = mid;
+    }
+    b = lo;
+    const int cu = __ldg(bt.cu + b);
+    const int q = min(__ldg(bt.cu + b + 1), bt.rows) - cu;
+    const long long first = (e - (static_cast<long long>(cu) * P.G / RT + b)) * RT;
+    if (q <= 0 || first >= static_cast<long long>(q) * P.G) return 0;
+    m0 = static_cast<int>(first);
+    const int n = held(bt, b, P.block, P.status);
+    const int last = min((m0 + RT - 1) / P.G, q - 1);
+    seen = P.causal ? min(max(n - (__ldg(bt.cu + b + 1) - cu) + last + 1, 0), n) : n;
+    if (m) {
+      m->cu = cu;
+      m->q = __ldg(bt.cu + b + 1) - cu;
+      m->n = n;
+    }
+    return max(1, (seen + kStep - 1) / kStep);
+  }
+};
+
+// The block's piece [lo, hi) of the line of steps, and the entry and offset of lo.
+template <int HD, int NT>
+__device__ void find_piece(const AttnParams& P, AttnSmem<HD, NT>& sm) {
+  const Entries<8 * NT> en{P};
+  const long long E = en.count();
+  const int mult = en.times();
+  const long long chunk = (E + kThreads - 1) / kThreads;
+  const long long e0 = min(E, threadIdx.x * chunk), e1 = min(E, e0 + chunk);
+  int b, m0, seen;
+  long long mine = 0;
+  for (long long e = e0; e < e1; ++e) mine += static_cast<long long>(en.steps(e, b, m0, seen, nullptr)) * mult;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sm.warp_total[warp] = incl;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += sm.warp_total[w];
+    total += sm.warp_total[w];
+  }
+  // at least two steps a block: a block's own costs are about one step's
+  const long long blocks = max(1ll, min(static_cast<long long>(gridDim.x), (total + 1) / 2));
+  const long long i = blockIdx.x;
+  const long long lo = i < blocks ? total * i / blocks : total;
+  const long long hi = i < blocks ? total * (i + 1) / blocks : total;
+  if (threadIdx.x == 0) {
+    sm.lo = lo;
+    sm.hi = hi;
+    sm.total = total;
+    sm.blocks = static_cast<int>(blocks);
+  }
+  long long at = before + incl - mine;
+  if (lo >= at && lo < at + mine) {
+    for (long long e = e0; e < e1; ++e) {
+      const long long n = static_cast<long long>(en.steps(e, b, m0, seen, nullptr)) * mult;
+      if (lo < at + n) {
+        sm.entry = static_cast<int>(e);
+        sm.rem = lo - at;
+        break;
+      }
+      at += n;
     }
   }
-  for (int e = 0; e < cnt; ++e) {
-    int pg = e;
-    if (list) {
-      pg = __ldg(list + e);
-      const bool good = pg > before && pg >= 0 && pg < held_pages;
-      before = pg;
-      if (!good) {
-        if (lane == 0) record_status(status, FVATTN_ERR_INVALID_ARG);
-        continue;
+  __syncthreads();
+}
+
+// Block that holds position x of the line: the last i with total i / blocks <= x.
+__device__ __forceinline__ int piece_of(long long x, long long total, int blocks) {
+  return static_cast<int>(((x + 1) * blocks - 1) / total);
+}
+
+template <typename T, int HD, int NT>
+__device__ void produce(const AttnParams& P, AttnSmem<HD, NT>& sm) {
+  using S = Shape<HD, NT>;
+  constexpr int RT = S::RT;
+  const int lane = threadIdx.x & 31;
+  volatile int* abort_flag = &sm.abort_flag;
+  const Entries<RT> en{P};
+  const long long E = en.count();
+  const int mult = en.times();
+  const int per = kStep / P.block;                 // pages per step
+  const int rec = Layout(HD, P.block).rec;
+  const long long total = sm.total, lo = sm.lo, hi = sm.hi;
+  long long entry = sm.entry, rem = sm.rem;
+  Meta m;
+  int b = 0, m0 = 0, seen = 0, steps = 0, s = 0, which = 0, cnt = 0, it = 0;
+  int window = -1, w_page = 0, w_slot = -1;        // 32 page positions of the unit, one a lane
+  bool fresh = true, ok = true;
+  for (long long x = lo; x < hi; ++x, ++it) {
+    bool first = false;
+    if (fresh) {                                   // the unit at position x
+      if (x == lo) {
+        steps = max(1, en.steps(entry, b, m0, seen, &m));
+        which = static_cast<int>(rem / steps);
+        s = static_cast<int>(rem - static_cast<long long>(which) * steps);
+      } else {
+        s = 0;
+        if (++which == mult) {
+          which = 0;
+          do ++entry; while (entry < E && en.steps(entry, b, m0, seen, nullptr) == 0);
+          if (entry >= E) {                        // lengths changed under the kernel
+            ok = false;
+            break;
+          }
+        }
+        steps = max(1, en.steps(entry, b, m0, seen, &m));
+      }
+      if (P.kv_idx) {
+        m.h = static_cast<int>(entry % P.c.H);
+        m.m0 = m0 + which * RT;
+        m.mc = min(RT, P.G - which * RT);
+        cnt = min(max(__ldg(P.kv_cnt + entry), 0), P.bt.max_pages);
+      } else {
+        m.h = which;
+        m.m0 = m0;
+        m.mc = static_cast<int>(min(static_cast<long long>(RT),
+                                    static_cast<long long>(min(m.q, P.bt.rows - m.cu)) * P.G - m0));
+        cnt = (seen + P.block - 1) / P.block;
+      }
+      m.seen = seen;
+      m.begin = piece_of(x - s, total, sm.blocks);
+      m.end = piece_of(x - s + steps - 1, total, sm.blocks);
+      window = -1;
+      first = true;
+      fresh = false;
+    }
+    int slot[2] = {-1, -1};
+    m.key0[0] = m.key0[1] = -1;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (k >= per) break;
+      const int pos = s * per + k;
+      if (pos >= cnt) break;
+      if ((pos >> 5) != window) {
+        window = pos >> 5;
+        const int p = window * 32 + lane;
+        w_page = p;
+        w_slot = -1;
+        if (p < cnt) {
+          bool good = true;
+          if (P.kv_idx) {
+            const int* list = P.kv_idx + entry * P.bt.max_pages;
+            w_page = __ldg(list + p);
+            good = w_page >= 0 && static_cast<long long>(w_page) * P.block < m.n && (p == 0 || w_page > __ldg(list + p - 1));
+            if (!good) record_status(P.status, FVATTN_ERR_INVALID_ARG);
+            good = good && w_page * P.block < seen;
+          }
+          if (good) w_slot = pool_slot(P.bt, P.c.num_pages, b, w_page, P.status);
+        }
+      }
+      slot[k] = __shfl_sync(0xffffffffu, w_slot, pos & 31);
+      const int page = __shfl_sync(0xffffffffu, w_page, pos & 31);
+      if (slot[k] >= 0) m.key0[k] = page * P.block;
+    }
+    m.first = first;
+    m.last = s + 1 == steps || x + 1 == hi;
+    const int st = it % S::kStages;
+    if (!__all_sync(0xffffffffu, mbar_wait(&sm.empty[st], ((it / S::kStages) & 1) ^ 1, abort_flag, P.status))) {
+      ok = false;
+      break;
+    }
+    if (lane == 0) {
+      sm.meta[st] = m;
+      const uint32_t bytes = ((slot[0] >= 0) + (slot[1] >= 0)) * rec;
+      if (bytes) mbar_arrive_expect_tx(&sm.full[st], bytes); else mbar_arrive(&sm.full[st]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (slot[k] >= 0)
+          bulk_load(sm.ring[st] + k * rec, P.c.pages + (static_cast<size_t>(slot[k]) * P.c.H + m.h) * rec, rec,
+                    &sm.full[st]);
+    }
+    __syncwarp();
+    if (++s == steps) fresh = true;
+  }
+  // every copy has landed before the block may end
+  if (!ok || hi > lo)
+    for (int o = max(0, it - S::kStages); o < it; ++o) mbar_wait_plain(&sm.full[o % S::kStages], (o / S::kStages) & 1);
+}
+
+template <typename T, int HD, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_stream_kernel(const AttnParams P) {
+  using S = Shape<HD, NT>;
+  constexpr int RT = S::RT;
+  constexpr bool kExact = sizeof(T) == 4;          // fp32: operands in two fp16 parts
+  constexpr int KS = HD / 16;                      // k-steps of S, and 16-channel tiles of O
+  constexpr int KW = HD / 32;                      // 32-bit words of K a lane and key
+  extern __shared__ uint8_t smem_raw[];
+  AttnSmem<HD, NT>& sm =
+      *reinterpret_cast<AttnSmem<HD, NT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &sm.abort_flag;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], kConsumers);
+    }
+    mbar_init(&sm.sync, kConsumers);
+    sm.abort_flag = 0;
+    fence_mbarrier_init();
+    if (blockIdx.x == 0 && __ldg(P.bt.cu + P.bt.B) > P.bt.rows) record_status(P.status, FVATTN_ERR_INVALID_ARG);
+  }
+  find_piece<HD, NT>(P, sm);                       // has block barriers
+  const int len = static_cast<int>(sm.hi - sm.lo);
+  if (len <= 0) return;
+  if (warp == kConsumers) {
+    produce<T, HD, NT>(P, sm);
+    return;
+  }
+
+  // ------------------------------------------------------------------ consumers
+  // All consumers meet here; bounded like every wait of the library, so that a lost
+  // warp cannot hold the others for good.
+  int met = 0;
+  auto meet = [&]() -> bool {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.sync);
+    return __all_sync(0xffffffffu, mbar_wait(&sm.sync, met++ & 1, abort_flag, P.status));
+  };
+  const int g = lane >> 2, t = lane & 3;
+  // Row g of a tile is the tile's key g ^ (g>>1 & 1): neighbouring lanes' V rows then lie
+  // in different halves of the banks.
+  const int gk = g ^ ((g >> 1) & 1);
+  const int ka = (2 * t) ^ (t & 1), kb = (2 * t + 1) ^ (t & 1);
+  const Layout L(HD, P.block);
+  const int pg = warp * 16 / P.block;              // page of the stage that holds the warp's keys
+  const int k_in = warp * 16 - pg * P.block;       // first of them inside the page
+  uint32_t qh[NT][KS][2], ql[kExact ? NT : 1][kExact ? KS : 1][2];
+  float o[NT][KS][4], mref[NT][2], l[NT][2], cs[NT][2];
+  int see[NT][2], unit_par = 0, all_seen = 0;
+  for (int it = 0; it < len; ++it) {
+    const int st = it % S::kStages;
+    if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[st], (it / S::kStages) & 1, abort_flag, P.status))) return;
+    const Meta& m = sm.meta[st];
+    if (m.first) {
+      const int mc = m.mc, m0 = m.m0, h = m.h, cu = m.cu, nq = m.q, n = m.n;
+      const float base = P.scale_log2 * (P.c.k_scale ? __ldg(P.c.k_scale + h) : 1.f);
+      all_seen = n;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int rr = j * 8 + g;                  // this lane's Q row
+        float v[HD / 4];
+#pragma unroll
+        for (int i = 0; i < HD / 4; ++i) v[i] = 0.f;
+        if (rr < mc) {
+          const int i = (m0 + rr) / P.G, gg = (m0 + rr) - i * P.G;
+          const T* src = static_cast<const T*>(P.q) + static_cast<long long>(cu + i) * P.q_stride +
+                         (static_cast<long long>(h) * P.G + gg) * HD + t * (HD / 4);
+          constexpr int E = 16 / sizeof(T);
+#pragma unroll
+          for (int k = 0; k < HD / 4 / E; ++k) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(src) + k);
+            const T* p = reinterpret_cast<const T*>(&w);
+#pragma unroll
+            for (int y = 0; y < E; ++y) v[k * E + y] = to_f(p[y]);
+          }
+        }
+        float mx = 0.f;
+#pragma unroll
+        for (int i = 0; i < HD / 4; ++i) mx = fmaxf(mx, fabsf(v[i]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // exponent that brings mx into [2^13, 2^14), in two factors so that neither overflows
+        int ex = 0;
+        if (mx > 0.f && mx <= FLT_MAX) ex = min(13 - ilogbf(mx), 126);
+        const float f1 = exp2f(static_cast<float>(ex / 2)), f2 = exp2f(static_cast<float>(ex - ex / 2));
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float a = v[4 * i + 2 * y] * f1 * f2, c = v[4 * i + 2 * y + 1] * f1 * f2;
+            qh[j][i][y] = pack2(a, c);
+            if constexpr (kExact) {
+              const float2 r = unpack2(qh[j][i][y]);
+              ql[j][i][y] = pack2(a - r.x, c - r.y);
+            }
+          }
+        }
+        // the columns of S^T that this lane holds: rows 2t and 2t+1 of the tile
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int col = 2 * t + y, c_row = j * 8 + col;
+          const int e = __shfl_sync(0xffffffffu, ex, col * 4);
+          // never 0: a masked key's -inf times it has to stay -inf
+          cs[j][y] = fmaxf(base * exp2f(static_cast<float>(-(e / 2))) * exp2f(static_cast<float>(-(e - e / 2))), FLT_MIN);
+          const int pos = n - nq + (m0 + c_row) / P.G;
+          see[j][y] = c_row < mc ? (P.causal ? min(max(pos + 1, 0), n) : n) : 0;
+          mref[j][y] = kFloor;
+          l[j][y] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) o[j][i][y] = 0.f;
+      }
+      all_seen = m.seen;
+    }
+    const int key0 = pg < 2 ? m.key0[pg] : -1;
+    const int kbase = key0 + k_in;                 // the warp's first key of the sequence
+    if (key0 >= 0 && kbase < all_seen) {           // warp-uniform
+      const uint8_t* rp = sm.ring[st] + pg * L.rec;
+      // ---- S^T
+      uint32_t kw[2][KW], ksc[2][2];               // K words and scales of the two keys
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int key = k_in + gk + 8 * y;
+        const uint8_t* p = rp + key * (HD / 2) + t * (HD / 8);
+        if constexpr (HD == 128) {
+          const uint4 w = *reinterpret_cast<const uint4*>(p);
+          kw[y][0] = w.x; kw[y][1] = w.y; kw[y][2] = w.z; kw[y][3] = w.w;
+          const uint32_t sc = e4m3x2(*reinterpret_cast<const uint16_t*>(rp + L.kscale() + key * 8 + 2 * t));
+          ksc[y][0] = __byte_perm(sc, 0, 0x1010);
+          ksc[y][1] = __byte_perm(sc, 0, 0x3232);
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2*>(p);
+          kw[y][0] = w.x; kw[y][1] = w.y;
+          const uint32_t sc = rp[L.kscale() + key * 4 + t];
+          ksc[y][0] = ksc[y][1] = e4m3x2(sc | (sc << 8));
+        }
+      }
+      float s[NT][4];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        uint32_t x[2][4];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          e2m1x8_to_half2(kw[y][w], x[y]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[y][i] = mul2(x[y][i], ksc[y][HD == 128 ? w / 2 : 0]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t a[4] = {x[0][2 * i], x[1][2 * i], x[0][2 * i + 1], x[1][2 * i + 1]};
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            mma_f16(s[j], a, qh[j][2 * w + i][0], qh[j][2 * w + i][1]);
+            if constexpr (kExact) mma_f16(s[j], a, ql[j][2 * w + i][0], ql[j][2 * w + i][1]);
+          }
+        }
+      }
+      // ---- V words of keys ka, kb and ka + 8, kb + 8, and their scales
+      constexpr int VW = HD / 64;                  // 32-bit words of a lane's HD/8 channels
+      uint32_t vw[4][VW], vsc[2];
+      {
+        uint32_t b[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int key = k_in + ((y & 1) ? kb : ka) + 8 * (y >> 1);
+          const uint8_t* p = rp + L.vcodes() + key * (HD / 2) + g * (HD / 16);
+          if constexpr (HD == 128) {
+            const uint2 w = *reinterpret_cast<const uint2*>(p);
+            vw[y][0] = w.x; vw[y][1] = w.y;
+            b[y] = rp[L.vscale() + key * 8 + g];
+          } else {
+            vw[y][0] = *reinterpret_cast<const uint32_t*>(p);
+            b[y] = rp[L.vscale() + key * 4 + (g >> 1)];
+          }
+          // behind the last key that a row sees the page holds anything, NaN scales too
+          if (kbase + key - k_in >= all_seen) b[y] = 0;
+        }
+        vsc[0] = e4m3x2(b[0] | (b[1] << 8));
+        vsc[1] = e4m3x2(b[2] | (b[3] << 8));
+      }
+      // ---- softmax: base-2 logits of keys gk, gk + 8 for rows 2t, 2t + 1 of each tile
+      uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          if (kbase + 15 >= see[j][y]) {           // some key is behind the row's last
+            if (kbase + gk >= see[j][y]) s[j][y] = -INFINITY;
+            if (kbase + gk + 8 >= see[j][y]) s[j][2 + y] = -INFINITY;
+          }
+        }
+        const float x0 = fmaxf(s[j][0], s[j][2]) * cs[j][0], x1 = fmaxf(s[j][1], s[j][3]) * cs[j][1];
+        // The max only has to be near: raised, for all keys of the warp, when it is
+        // exceeded by 2^8.
+        const bool raise = x0 > mref[j][0] + (kHead + kRaise) || x1 > mref[j][1] + (kHead + kRaise);
+        if (__any_sync(0xffffffffu, raise)) {
+          float mx[2] = {x0, x1};
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) {
+            mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], d));
+            mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], d));
+          }
+          float f[2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float nm = fmaxf(mref[j][y], mx[y] - kHead);
+            f[y] = ex2_approx(mref[j][y] - nm);
+            mref[j][y] = nm;
+            l[j][y] *= f[y];
+          }
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            o[j][i][0] *= f[0];
+            o[j][i][1] *= f[1];
+            o[j][i][2] *= f[0];
+            o[j][i][3] *= f[1];
+          }
+        }
+        float p[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) p[y] = ex2_approx(fmaf(s[j][y], cs[j][y & 1], -mref[j][y & 1]));
+        l[j][0] += p[0] + p[2];
+        l[j][1] += p[1] + p[3];
+        const uint32_t h0 = pack2(p[0], p[1]), h1 = pack2(p[2], p[3]);
+        ph[j][0] = transpose8x8(h0);
+        ph[j][1] = transpose8x8(h1);
+        if constexpr (kExact) {
+          const float2 r0 = unpack2(h0), r1 = unpack2(h1);
+          pl[j][0] = transpose8x8(pack2(p[0] - r0.x, p[1] - r0.y));
+          pl[j][1] = transpose8x8(pack2(p[2] - r1.x, p[3] - r1.y));
+        }
+      }
+      // ---- O^T
+#pragma unroll
+      for (int w = 0; w < VW; ++w) {
+        // two keys' codes of one channel side by side: the even channels, the odd ones
+        uint32_t x[4][4];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t a = vw[2 * y][w], b = vw[2 * y + 1][w];
+          e2m1x8_to_half2((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), x[2 * y]);
+          e2m1x8_to_half2(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), x[2 * y + 1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t a[4] = {mul2(x[0][i], vsc[0]), mul2(x[1][i], vsc[0]), mul2(x[2][i], vsc[1]),
+                                 mul2(x[3][i], vsc[1])};
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            if constexpr (kExact) {
+              float d[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_f16(d, a, pl[j][0], pl[j][1]);
+              mma_f16(d, a, ph[j][0], ph[j][1]);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) o[j][4 * w + i][y] += d[y];
+            } else {
+              mma_f16(o[j][4 * w + i], a, ph[j][0], ph[j][1]);
+            }
+          }
+        }
       }
     }
-    if (pg >= pages) continue;
-    const int slot = pool_slot(bt, c.num_pages, b, pg, status);
-    if (slot < 0) continue;
-    const uint8_t* rec = c.pages + (static_cast<size_t>(slot) * c.H + h) * L.rec;
-    const int keys = min(block, seen - pg * block);
-    for (int t = 0; t < keys; ++t) {
-      const int ch = lane * C;
-      auto value = [&](int codes, int scales, int i) {
-        const uint8_t byte = rec[codes + t * (HD / 2) + ((ch + i) >> 1)];
-        const uint32_t w = ((ch + i) & 1) ? byte >> 4 : byte & 15;
-        uint32_t p[4];
-        e2m1x8_to_half2(w, p);
-        return __low2float(*reinterpret_cast<__half2*>(&p[0])) *
-               e4m3_to_float(rec[scales + t * (HD / kGroup) + (ch + i) / kGroup]);
-      };
-      float s = 0.f;
+    const bool last = m.last;
+    if (!last) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[st]);
+      continue;
+    }
+    // ------------------------------------------------------------ end of the unit's piece
+    const int mc = m.mc, m0 = m.m0, h = m.h, cu = m.cu, begin = m.begin, end = m.end;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.empty[st]);
+    const int par = unit_par++ & 1;
 #pragma unroll
-      for (int i = 0; i < C; ++i) s = fmaf(qv[i], value(0, L.kscale(), i), s);
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-      const float mn = fmaxf(m, s);
-      const float f = __expf(m - mn), pr = __expf(s - mn);
-      m = mn;
-      l = l * f + pr;
+      for (int y = 0; y < 2; ++y) {
 #pragma unroll
-      for (int i = 0; i < C; ++i) o[i] = fmaf(pr, value(L.vcodes(), L.vscale(), i), o[i] * f);
+        for (int d = 4; d < 32; d <<= 1) l[j][y] += __shfl_xor_sync(0xffffffffu, l[j][y], d);
+        if (g == 0) {
+          sm.mx[par][warp][j * 8 + 2 * t + y] = mref[j][y];
+          sm.sum[par][warp][j * 8 + 2 * t + y] = l[j][y];
+        }
+      }
+    if (!meet()) return;
+    float f[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        float mx = kFloor;
+        for (int w = 0; w < kConsumers; ++w) mx = fmaxf(mx, sm.mx[par][w][j * 8 + 2 * t + y]);
+        f[j][y] = ex2_approx(mref[j][y] - mx);
+      }
+    // lane's channels (HD/8) g + 2 i, + 1 of rows 2t, 2t + 1
+    auto each = [&](auto&& fn) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            fn(j * 8 + 2 * t + y, g * (HD / 8) + 2 * i, o[j][i][y], o[j][i][2 + y], f[j][y]);
+    };
+    if (warp >= 4)
+      each([&](int row, int ch, float a, float b, float fac) {
+        *reinterpret_cast<float2*>(&sm.slab[warp - 4][row][ch]) = make_float2(a * fac, b * fac);
+      });
+    if (!meet()) return;
+    if (warp < 4)
+      each([&](int row, int ch, float a, float b, float fac) {
+        float2* p = reinterpret_cast<float2*>(&sm.slab[warp][row][ch]);
+        const float2 v = *p;
+        *p = make_float2(fmaf(a, fac, v.x), fmaf(b, fac, v.y));
+      });
+    if (!meet()) return;
+    const bool whole = begin == end;
+    float* mine = P.part + (static_cast<size_t>(blockIdx.x) * 2 + (begin == static_cast<int>(blockIdx.x) ? 1 : 0)) * S::kPart;
+    const float vs = P.c.v_scale ? __ldg(P.c.v_scale + h) : 1.f;
+    constexpr int kPer = RT * HD / 4 / (kConsumers * 32);   // float4 a thread
+    static_assert(RT * HD / 4 % (kConsumers * 32) == 0 || RT * HD / 4 < kConsumers * 32, "");
+    auto finish = [&](int row, int ch, float4 v, float mx, float sum) {
+      if (row >= mc) return;
+      const int i = (m0 + row) / P.G, gg = (m0 + row) - i * P.G;
+      const size_t at = (static_cast<size_t>(cu + i) * P.c.H * P.G + static_cast<size_t>(h) * P.G + gg);
+      const float inv = sum > 0.f || sum != sum ? vs / sum : 0.f;
+      T* dst = static_cast<T*>(P.out) + at * HD + ch;
+      if constexpr (kExact) {
+        *reinterpret_cast<float4*>(dst) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+      } else {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+      }
+      if (P.lse && ch == 0) P.lse[at] = sum > 0.f || sum != sum ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+    };
+#pragma unroll
+    for (int k = 0; k < (kPer > 0 ? kPer : 1); ++k) {
+      const int at = (threadIdx.x + k * kConsumers * 32) * 4;
+      if (at >= RT * HD) break;
+      const int row = at / HD, ch = at % HD;
+      float mx = kFloor;
+      for (int w = 0; w < kConsumers; ++w) mx = fmaxf(mx, sm.mx[par][w][row]);
+      float sum = 0.f;
+      for (int w = 0; w < kConsumers; ++w) sum += sm.sum[par][w][row] * ex2_approx(sm.mx[par][w][row] - mx);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float4 a = *reinterpret_cast<const float4*>(&sm.slab[w][row][ch]);
+        v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
+      }
+      if (whole) {
+        finish(row, ch, v, mx, sum);
+      } else {
+        *reinterpret_cast<float4*>(mine + row * HD + ch) = v;
+        if (ch == 0) {
+          mine[RT * HD + row] = mx;
+          mine[RT * HD + RT + row] = sum;
+        }
+      }
+    }
+    if (whole) continue;
+    // ---- the unit lies in blocks begin .. end: the last to arrive joins them in order
+    __threadfence();
+    if (!meet()) return;
+    if (threadIdx.x == 0) {
+      sm.joiner = atomicAdd(P.arrived + begin, 1) == end - begin;
+      __threadfence();
+    }
+    if (!meet()) return;
+    if (!sm.joiner) continue;
+    __threadfence();
+    auto part_of = [&](int i) {
+      return P.part + (static_cast<size_t>(i) * 2 + (i == begin ? 1 : 0)) * S::kPart;
+    };
+#pragma unroll
+    for (int k = 0; k < (kPer > 0 ? kPer : 1); ++k) {
+      const int at = (threadIdx.x + k * kConsumers * 32) * 4;
+      if (at >= RT * HD) break;
+      const int row = at / HD, ch = at % HD;
+      if (row >= mc) continue;
+      float mx = kFloor;
+      for (int i = begin; i <= end; ++i) mx = fmaxf(mx, __ldcg(part_of(i) + RT * HD + row));
+      float sum = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int i = begin; i <= end; ++i) {
+        const float* p = part_of(i);
+        const float fac = ex2_approx(__ldcg(p + RT * HD + row) - mx);
+        const float4 a = __ldcg(reinterpret_cast<const float4*>(p + row * HD + ch));
+        sum = fmaf(__ldcg(p + RT * HD + RT + row), fac, sum);
+        v.x = fmaf(a.x, fac, v.x); v.y = fmaf(a.y, fac, v.y);
+        v.z = fmaf(a.z, fac, v.z); v.w = fmaf(a.w, fac, v.w);
+      }
+      finish(row, ch, v, mx, sum);
     }
   }
-  const float inv = l > 0.f ? (c.v_scale ? __ldg(c.v_scale + h) : 1.f) / l : 0.f;
-#pragma unroll
-  for (int i = 0; i < C; ++i) out[static_cast<size_t>(unit) * HD + lane * C + i] = static_cast<T>(o[i] * inv);
-  if (lse && lane == 0) lse[unit] = l > 0.f ? m + logf(l) : -INFINITY;
+}
+
+// Workspace behind the header: arrival counters, then partial results.
+constexpr int kMaxBlocks = 512;                    // two blocks on each of 148 SMs, and room
+
+size_t attn_ws_bytes(int d) {
+  const size_t part = 16 * d + 32;
+  return kMaxBlocks * sizeof(int) + static_cast<size_t>(kMaxBlocks) * 2 * part * sizeof(float);
+}
+// Bytes behind the header that a call clears.
+size_t attn_ws_clear() { return kMaxBlocks * sizeof(int); }
+
+template <typename T, int HD, int NT>
+static cudaError_t launch_stream(const AttnParams& P, int num_sms, cudaStream_t st) {
+  const int smem = static_cast<int>(sizeof(AttnSmem<HD, NT>)) + 128;
+  cudaError_t e = cudaFuncSetAttribute(attn_stream_kernel<T, HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int grid = min(kMaxBlocks, num_sms * (NT == 1 ? 2 : 1));
+  attn_stream_kernel<T, HD, NT><<<grid, kThreads, smem, st>>>(P);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_attn(const Cache& c, const Batch& bt, const void* q, long long q_stride, int Hq, void* out,
-                        float* lse, bool bf16, float scale, int causal, int d, int block, const int* kv_idx,
-                        const int* kv_cnt, int* status, cudaStream_t st) {
-  const long long grid = (static_cast<long long>(bt.rows) * Hq + 3) / 4;
-  if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-#define FVATTN_KV4_ATTN(T, HD)                                                                                  \
-  attn_kernel<T, HD><<<static_cast<unsigned>(grid), 128, 0, st>>>(c, bt, static_cast<const T*>(q), q_stride, Hq, \
-                                                                  static_cast<T*>(out), lse, scale, causal,      \
-                                                                  block, kv_idx, kv_cnt, status)
-  if (bf16) {
-    if (d == 128) FVATTN_KV4_ATTN(__nv_bfloat16, 128); else FVATTN_KV4_ATTN(__nv_bfloat16, 64);
-  } else {
-    if (d == 128) FVATTN_KV4_ATTN(float, 128); else FVATTN_KV4_ATTN(float, 64);
-  }
-#undef FVATTN_KV4_ATTN
-  return cudaGetLastError();
+                        float* lse, bool bf16, float scale, int causal, int d, int block, int max_q, const int* kv_idx,
+                        const int* kv_cnt, int* status, uint8_t* ws, int num_sms, cudaStream_t st) {
+  AttnParams P;
+  P.c = c;
+  P.bt = bt;
+  P.q = q;
+  P.q_stride = q_stride;
+  P.out = out;
+  P.lse = lse;
+  P.kv_idx = kv_idx;
+  P.kv_cnt = kv_cnt;
+  P.scale_log2 = scale * 1.4426950408889634f;
+  P.G = Hq / c.H;
+  P.causal = causal;
+  P.block = block;
+  P.status = status;
+  P.arrived = reinterpret_cast<int*>(ws);
+  P.part = reinterpret_cast<float*>(ws + attn_ws_clear());
+  // Eight query rows a unit leave two blocks on an SM; more rows than that take sixteen.
+  const bool few = (kv_idx ? P.G : static_cast<long long>(max_q) * P.G) <= 8;
+#define FVATTN_KV4(T, HD) (few ? launch_stream<T, HD, 1>(P, num_sms, st) : launch_stream<T, HD, 2>(P, num_sms, st))
+  if (bf16) return d == 128 ? FVATTN_KV4(__nv_bfloat16, 128) : FVATTN_KV4(__nv_bfloat16, 64);
+  return d == 128 ? FVATTN_KV4(float, 128) : FVATTN_KV4(float, 64);
+#undef FVATTN_KV4
 }
 
 }  // namespace kv4

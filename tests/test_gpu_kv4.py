@@ -53,7 +53,7 @@ class Case:
         self.ks, self.vs = sc(), sc()
         up = lambda t: None if t is None else t.to(dev)
         self.cache = F.KV4Cache(slots, H, d, block, dev, k_scale=up(self.ks), v_scale=up(self.vs))
-        self.cache.pages.fill_(0x77)                        # what was never written is large
+        self.cache.pages.fill_(0xFF)                        # what was never written has NaN scales
         self.table = table.to(dev)
         rnd = lambda n: spread * torch.randn((n, H, d), generator=self.g)
         self.k = [rnd(n).to(dtype) for n in kv]
@@ -184,7 +184,7 @@ def test_codes_scales_and_sums_are_exact(kv, H, d, block, scaled, dtype):
     for b, n in enumerate(kv):
         for t in range(n):
             owned[c.table_np[b, t // block], t % block] = True
-    assert np.all(kc.transpose(0, 2, 1, 3)[~owned] == 7) and np.all(vs.transpose(0, 2, 1, 3)[~owned] == 0x77)
+    assert np.all(kc.transpose(0, 2, 1, 3)[~owned] == 15) and np.all(vs.transpose(0, 2, 1, 3)[~owned] == 0xFF)
 
 
 @pytest.mark.parametrize("steps", [[1] * 9, [5, 64, 1, 60, 3], [127, 1, 2], [200]])
