@@ -18,7 +18,7 @@ cudaError_t launch_select(const Cache& c, const Batch& bt, const void* q, long l
 cudaError_t launch_attn(const Cache& c, const Batch& bt, const void* q, long long q_stride, int Hq, void* out,
                         float* lse, bool bf16, float scale, int causal, int d, int block, int max_q, const int* kv_idx,
                         const int* kv_cnt, int* status, uint8_t* ws, int num_sms, cudaStream_t st);
-size_t attn_ws_bytes(int d);
+size_t attn_ws_bytes(int d, int max_q, int G);
 size_t attn_ws_clear();
 }  // namespace kv4
 }  // namespace fvattn
@@ -119,7 +119,8 @@ size_t fvattn_kv4_workspace_bytes(fvattn_op op, const fvattn_kv4_cache* cache, c
     case FVATTN_OP_KV4_SELECT:
       return valid_heads(cache, Hq) && batch->max_pages <= kMaxSelectPages ? kWsHeaderBytes : 0;
     case FVATTN_OP_KV4_ATTN:
-      return valid_heads(cache, Hq) ? kWsHeaderBytes + fvattn::align_up(fvattn::kv4::attn_ws_bytes(cache->d), 256) : 0;
+      if (!valid_heads(cache, Hq)) return 0;
+      return kWsHeaderBytes + fvattn::align_up(fvattn::kv4::attn_ws_bytes(cache->d, batch->max_q, Hq / cache->H), 256);
     default: return 0;
   }
 }

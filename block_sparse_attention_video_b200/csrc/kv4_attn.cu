@@ -2,14 +2,7 @@
 // drafts, selected pages, and every fp32 call. One pass over the cache with the running
 // maximum and sum of the softmax, split over the pages and joined in a fixed order.
 //
-// Unit: up to RT = 8 NT query rows (a sequence's (row, query head) pairs that share a KV
-// head, in that order; with lists, the query heads of one row) against the pages they
-// see. A step is 128 keys: one page of 128 tokens or two of 64. The steps of all units
-// form one line that is cut into equal pieces, one per block, so ragged lengths balance
-// by themselves: every block adds up the units' lengths and finds its piece. A unit that
-// lies in several pieces leaves partial sums in the workspace; the block that arrives
-// last joins them in the order of the pieces, so the result does not depend on who that
-// is.
+// Units of up to 8 NT query rows, cut into equal pieces over the blocks (kv4_units.cuh).
 //
 // A block is one producer warp, which brings whole page records into a ring of shared
 // memory (one bulk copy a page, 18 KB at d 128), and eight consumer warps with 16 keys of
@@ -33,7 +26,7 @@
 // rounded.
 #include <cfloat>
 
-#include "kv4.cuh"
+#include "kv4_units.cuh"
 #include "sm100.cuh"
 
 namespace fvattn {
@@ -41,40 +34,7 @@ namespace kv4 {
 
 constexpr int kConsumers = 8;                       // consumer warps, 16 keys each
 constexpr int kThreads = (kConsumers + 1) * 32;
-constexpr int kStep = kConsumers * 16;              // keys per step
-constexpr float kFloor = -3.0e38f;                  // running max before any key
-constexpr float kRaise = 8.f;                       // the max is raised when exceeded by 2^8
-constexpr float kHead = 6.f;                        // P <= 2^(6 + 8) stays inside fp16
-constexpr float kLn2 = 0.69314718055994531f;
-
-struct AttnParams {
-  Cache c;
-  Batch bt;
-  const void* q;
-  long long q_stride;
-  void* out;
-  float* lse;
-  const int* kv_idx;      // nullptr: every page
-  const int* kv_cnt;
-  float scale_log2;       // scale * log2(e)
-  int G, causal, block;
-  int* status;
-  int* arrived;           // [gridDim] blocks that left their part of the unit begun there
-  float* part;            // [gridDim][2] partial sums: O [RT][HD], max [RT], sum [RT]
-};
-
-// A unit and the piece of it that a step belongs to, published with each stage.
-struct Meta {
-  int key0[2];            // first key of the stage's pages; -1: no such page
-  int first, last;        // first / last step of the unit in this block
-  int cu, q, n;           // the sequence: first row, rows, tokens held
-  int m0, mc;             // first (row, head) pair and their number
-  int h;                  // KV head
-  int seen;               // keys that the unit's last row sees
-  int begin, end;         // blocks that hold the unit's first and last step
-  int pad[3];
-};
-static_assert(sizeof(Meta) == 64, "sixteen words, written by sixteen lanes");
+static_assert(kStep == kConsumers * 16, "");
 
 template <int HD, int NT>
 struct Shape {
@@ -96,20 +56,10 @@ struct __align__(128) AttnSmem {
   uint64_t full[S::kStages];
   uint64_t empty[S::kStages];
   uint64_t sync;
-  long long warp_total[kThreads / 32];
-  long long lo, hi, rem, total;
-  int entry, blocks;
+  Piece piece;
   int joiner;
   int abort_flag;
 };
-
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -141,118 +91,6 @@ __device__ __forceinline__ uint32_t e4m3x2(uint32_t two_codes) {
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(float x) { return x; }
 
-// Entries are what the units are counted by: without lists, tiles of RT pairs of a
-// sequence (each counts for all KV heads); with lists, (row, KV head) (each counts for
-// all tiles of its query heads). Tiles are numbered without a prefix sum: sequence b owns
-// those from cu[b] G / RT + b on, room for the at most ceil(q G / RT) it needs.
-template <int RT>
-struct Entries {
-  const AttnParams& P;
-  __device__ long long count() const {
-    return P.kv_idx ? static_cast<long long>(P.bt.rows) * P.c.H
-                    : static_cast<long long>(P.bt.rows) * P.G / RT + P.bt.B;
-  }
-  __device__ int times() const { return P.kv_idx ? (P.G + RT - 1) / RT : P.c.H; }
-  // Steps of a unit of entry e and where it lies; 0 if the entry is not in use.
-  __device__ int steps(long long e, int& b, int& m0, int& seen, Meta* m) const {
-    const Batch& bt = P.bt;
-    if (P.kv_idx) {
-      const int r = static_cast<int>(e / P.c.H);
-      if (!sequence_of(bt, r, b)) return 0;
-      int cnt = __ldg(P.kv_cnt + e);
-      if (cnt < 0 || cnt > bt.max_pages) {
-        record_status(P.status, FVATTN_ERR_INVALID_ARG);
-        cnt = min(max(cnt, 0), bt.max_pages);
-      }
-      m0 = (r - __ldg(bt.cu + b)) * P.G;
-      if (m) {
-        m->cu = __ldg(bt.cu + b);
-        m->q = __ldg(bt.cu + b + 1) - m->cu;
-        m->n = held(bt, b, P.block, P.status);
-        const int pos = m->n - m->q + (r - m->cu);
-        seen = P.causal ? min(max(pos + 1, 0), m->n) : m->n;
-      }
-      return max(1, (cnt * P.block + kStep - 1) / kStep);
-    }
-    int lo = 0, hi = bt.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (static_cast<long long>(__ldg(bt.cu + mid)) * P.G / RT + mid <= e) lo = mid; else hi = mid;
-    }
-    b = lo;
-    const int cu = __ldg(bt.cu + b);
-    const int q = min(__ldg(bt.cu + b + 1), bt.rows) - cu;
-    const long long first = (e - (static_cast<long long>(cu) * P.G / RT + b)) * RT;
-    if (q <= 0 || first >= static_cast<long long>(q) * P.G) return 0;
-    m0 = static_cast<int>(first);
-    const int n = held(bt, b, P.block, P.status);
-    const int last = min((m0 + RT - 1) / P.G, q - 1);
-    seen = P.causal ? min(max(n - (__ldg(bt.cu + b + 1) - cu) + last + 1, 0), n) : n;
-    if (m) {
-      m->cu = cu;
-      m->q = __ldg(bt.cu + b + 1) - cu;
-      m->n = n;
-    }
-    return max(1, (seen + kStep - 1) / kStep);
-  }
-};
-
-// The block's piece [lo, hi) of the line of steps, and the entry and offset of lo.
-template <int HD, int NT>
-__device__ void find_piece(const AttnParams& P, AttnSmem<HD, NT>& sm) {
-  const Entries<8 * NT> en{P};
-  const long long E = en.count();
-  const int mult = en.times();
-  const long long chunk = (E + kThreads - 1) / kThreads;
-  const long long e0 = min(E, threadIdx.x * chunk), e1 = min(E, e0 + chunk);
-  int b, m0, seen;
-  long long mine = 0;
-  for (long long e = e0; e < e1; ++e) mine += static_cast<long long>(en.steps(e, b, m0, seen, nullptr)) * mult;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) sm.warp_total[warp] = incl;
-  __syncthreads();
-  long long before = 0, total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += sm.warp_total[w];
-    total += sm.warp_total[w];
-  }
-  // at least two steps a block: a block's own costs are about one step's
-  const long long blocks = max(1ll, min(static_cast<long long>(gridDim.x), (total + 1) / 2));
-  const long long i = blockIdx.x;
-  const long long lo = i < blocks ? total * i / blocks : total;
-  const long long hi = i < blocks ? total * (i + 1) / blocks : total;
-  if (threadIdx.x == 0) {
-    sm.lo = lo;
-    sm.hi = hi;
-    sm.total = total;
-    sm.blocks = static_cast<int>(blocks);
-  }
-  long long at = before + incl - mine;
-  if (lo >= at && lo < at + mine) {
-    for (long long e = e0; e < e1; ++e) {
-      const long long n = static_cast<long long>(en.steps(e, b, m0, seen, nullptr)) * mult;
-      if (lo < at + n) {
-        sm.entry = static_cast<int>(e);
-        sm.rem = lo - at;
-        break;
-      }
-      at += n;
-    }
-  }
-  __syncthreads();
-}
-
-// Block that holds position x of the line: the last i with total i / blocks <= x.
-__device__ __forceinline__ int piece_of(long long x, long long total, int blocks) {
-  return static_cast<int>(((x + 1) * blocks - 1) / total);
-}
-
 template <typename T, int HD, int NT>
 __device__ void produce(const AttnParams& P, AttnSmem<HD, NT>& sm) {
   using S = Shape<HD, NT>;
@@ -264,8 +102,8 @@ __device__ void produce(const AttnParams& P, AttnSmem<HD, NT>& sm) {
   const int mult = en.times();
   const int per = kStep / P.block;                 // pages per step
   const int rec = Layout(HD, P.block).rec;
-  const long long total = sm.total, lo = sm.lo, hi = sm.hi;
-  long long entry = sm.entry, rem = sm.rem;
+  const long long total = sm.piece.total, lo = sm.piece.lo, hi = sm.piece.hi;
+  long long entry = sm.piece.entry, rem = sm.piece.rem;
   Meta m;
   int b = 0, m0 = 0, seen = 0, steps = 0, s = 0, which = 0, cnt = 0, it = 0;
   int window = -1, w_page = 0, w_slot = -1;        // 32 page positions of the unit, one a lane
@@ -302,8 +140,8 @@ __device__ void produce(const AttnParams& P, AttnSmem<HD, NT>& sm) {
         cnt = (seen + P.block - 1) / P.block;
       }
       m.seen = seen;
-      m.begin = piece_of(x - s, total, sm.blocks);
-      m.end = piece_of(x - s + steps - 1, total, sm.blocks);
+      m.begin = piece_of(x - s, total, sm.piece.blocks);
+      m.end = piece_of(x - s + steps - 1, total, sm.piece.blocks);
       window = -1;
       first = true;
       fresh = false;
@@ -383,8 +221,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_stream_kernel(
     fence_mbarrier_init();
     if (blockIdx.x == 0 && __ldg(P.bt.cu + P.bt.B) > P.bt.rows) record_status(P.status, FVATTN_ERR_INVALID_ARG);
   }
-  find_piece<HD, NT>(P, sm);                       // has block barriers
-  const int len = static_cast<int>(sm.hi - sm.lo);
+  find_piece<RT, kThreads>(P, sm.piece, 2);        // a block's own costs are about one step's
+  const int len = static_cast<int>(sm.piece.hi - sm.piece.lo);
   if (len <= 0) return;
   if (warp == kConsumers) {
     produce<T, HD, NT>(P, sm);
@@ -764,14 +602,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_stream_kernel(
 }
 
 // Workspace behind the header: arrival counters, then partial results.
-constexpr int kMaxBlocks = 512;                    // two blocks on each of 148 SMs, and room
+constexpr int kMaxBlocks = 320;                    // two blocks on each of 148 SMs, and room
+constexpr int kMaxChunkBlocks = 160;
 
-size_t attn_ws_bytes(int d) {
-  const size_t part = 16 * d + 32;
-  return kMaxBlocks * sizeof(int) + static_cast<size_t>(kMaxBlocks) * 2 * part * sizeof(float);
-}
+size_t chunk_part_bytes(int d, int grid);
+cudaError_t launch_chunk(const AttnParams& P, int d, int grid, cudaStream_t st);
+
+// Where the tensor cores' 128-row tiles take over (the fp32 path and lists stay here).
+static bool many_rows(int max_q, int G) { return static_cast<long long>(max_q) * G > 16; }
+
 // Bytes behind the header that a call clears.
 size_t attn_ws_clear() { return kMaxBlocks * sizeof(int); }
+size_t attn_ws_bytes(int d, int max_q, int G) {
+  const size_t few = static_cast<size_t>(kMaxBlocks) * 2 * (16 * d + 32) * sizeof(float);
+  const size_t part = many_rows(max_q, G) ? max(few, chunk_part_bytes(d, kMaxChunkBlocks)) : few;
+  return attn_ws_clear() + part;
+}
 
 template <typename T, int HD, int NT>
 static cudaError_t launch_stream(const AttnParams& P, int num_sms, cudaStream_t st) {
@@ -802,6 +648,7 @@ cudaError_t launch_attn(const Cache& c, const Batch& bt, const void* q, long lon
   P.status = status;
   P.arrived = reinterpret_cast<int*>(ws);
   P.part = reinterpret_cast<float*>(ws + attn_ws_clear());
+  if (bf16 && !kv_idx && many_rows(max_q, P.G)) return launch_chunk(P, d, min(kMaxChunkBlocks, num_sms), st);
   // Eight query rows a unit leave two blocks on an SM; more rows than that take sixteen.
   const bool few = (kv_idx ? P.G : static_cast<long long>(max_q) * P.G) <= 8;
 #define FVATTN_KV4(T, HD) (few ? launch_stream<T, HD, 1>(P, num_sms, st) : launch_stream<T, HD, 2>(P, num_sms, st))

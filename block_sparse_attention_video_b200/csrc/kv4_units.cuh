@@ -1,0 +1,172 @@
+// kv4_units.cuh -- how the attention kernels of the 4-bit cache divide their work.
+//
+// Unit: up to RT query rows (a sequence's (row, query head) pairs that share a KV head, in
+// that order; with lists, the query heads of one row) against the pages they see. A step is
+// 128 keys: one page of 128 tokens or two of 64. The steps of all units form one line that is
+// cut into equal pieces, one per block, so ragged and causal lengths balance by themselves:
+// every block adds up the units' lengths and finds its piece. A unit that lies in several
+// pieces leaves partial sums in the workspace; the block that arrives last joins them in the
+// order of the pieces, so the result does not depend on who that is.
+#pragma once
+
+#include "kv4.cuh"
+
+namespace fvattn {
+namespace kv4 {
+
+constexpr int kStep = 128;                          // keys per step
+constexpr float kFloor = -3.0e38f;                  // running max before any key
+constexpr float kRaise = 8.f;                       // the max is raised when exceeded by 2^8
+constexpr float kHead = 6.f;                        // P <= 2^(6 + 8) stays inside fp16
+constexpr float kLn2 = 0.69314718055994531f;
+
+struct AttnParams {
+  Cache c;
+  Batch bt;
+  const void* q;
+  long long q_stride;
+  void* out;
+  float* lse;
+  const int* kv_idx;      // nullptr: every page
+  const int* kv_cnt;
+  float scale_log2;       // scale * log2(e)
+  int G, causal, block;
+  int* status;
+  int* arrived;           // [gridDim] blocks that left their part of the unit begun there
+  float* part;            // partial results of units that lie in several blocks
+};
+
+// A unit, as its producer publishes it to the other warps.
+struct Meta {
+  int key0[2];            // first key of the step's pages; -1: no such page
+  int first, last;        // first / last step of the unit in this block
+  int cu, q, n;           // the sequence: first row, rows, tokens held
+  int m0, mc;             // first (row, head) pair and their number
+  int h;                  // KV head
+  int seen;               // keys that the unit's last row sees
+  int begin, end;         // blocks that hold the unit's first and last step
+  int s0, ns;             // first of the unit's steps in this block, and their number
+  int pad;
+};
+
+// Entries are what the units are counted by: without lists, tiles of RT pairs of a
+// sequence (each counts for all KV heads); with lists, (row, KV head) (each counts for
+// all tiles of its query heads). Tiles are numbered without a prefix sum: sequence b owns
+// those from cu[b] G / RT + b on, room for the at most ceil(q G / RT) it needs.
+template <int RT>
+struct Entries {
+  const AttnParams& P;
+  __device__ long long count() const {
+    return P.kv_idx ? static_cast<long long>(P.bt.rows) * P.c.H
+                    : static_cast<long long>(P.bt.rows) * P.G / RT + P.bt.B;
+  }
+  __device__ int times() const { return P.kv_idx ? (P.G + RT - 1) / RT : P.c.H; }
+  // Steps of a unit of entry e and where it lies; 0 if the entry is not in use.
+  __device__ int steps(long long e, int& b, int& m0, int& seen, Meta* m) const {
+    const Batch& bt = P.bt;
+    if (P.kv_idx) {
+      const int r = static_cast<int>(e / P.c.H);
+      if (!sequence_of(bt, r, b)) return 0;
+      int cnt = __ldg(P.kv_cnt + e);
+      if (cnt < 0 || cnt > bt.max_pages) {
+        record_status(P.status, FVATTN_ERR_INVALID_ARG);
+        cnt = min(max(cnt, 0), bt.max_pages);
+      }
+      m0 = (r - __ldg(bt.cu + b)) * P.G;
+      if (m) {
+        m->cu = __ldg(bt.cu + b);
+        m->q = __ldg(bt.cu + b + 1) - m->cu;
+        m->n = held(bt, b, P.block, P.status);
+        const int pos = m->n - m->q + (r - m->cu);
+        seen = P.causal ? min(max(pos + 1, 0), m->n) : m->n;
+      }
+      return max(1, (cnt * P.block + kStep - 1) / kStep);
+    }
+    int lo = 0, hi = bt.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (static_cast<long long>(__ldg(bt.cu + mid)) * P.G / RT + mid <= e) lo = mid; else hi = mid;
+    }
+    b = lo;
+    const int cu = __ldg(bt.cu + b);
+    const int q = min(__ldg(bt.cu + b + 1), bt.rows) - cu;
+    const long long first = (e - (static_cast<long long>(cu) * P.G / RT + b)) * RT;
+    if (q <= 0 || first >= static_cast<long long>(q) * P.G) return 0;
+    m0 = static_cast<int>(first);
+    const int n = held(bt, b, P.block, P.status);
+    const int last = min((m0 + RT - 1) / P.G, q - 1);
+    seen = P.causal ? min(max(n - (__ldg(bt.cu + b + 1) - cu) + last + 1, 0), n) : n;
+    if (m) {
+      m->cu = cu;
+      m->q = __ldg(bt.cu + b + 1) - cu;
+      m->n = n;
+    }
+    return max(1, (seen + kStep - 1) / kStep);
+  }
+};
+
+// The block's piece [lo, hi) of the line of steps, and the entry and offset of lo.
+struct Piece {
+  long long warp_total[32];
+  long long lo, hi, rem, total;
+  int entry, blocks;
+};
+
+// Called by all threads of the block (has block barriers); at least `least` steps go to a
+// block that gets any.
+template <int RT, int kThreads>
+__device__ void find_piece(const AttnParams& P, Piece& sm, int least) {
+  const Entries<RT> en{P};
+  const long long E = en.count();
+  const int mult = en.times();
+  const long long chunk = (E + kThreads - 1) / kThreads;
+  const long long e0 = min(E, threadIdx.x * chunk), e1 = min(E, e0 + chunk);
+  int b, m0, seen;
+  long long mine = 0;
+  for (long long e = e0; e < e1; ++e) mine += static_cast<long long>(en.steps(e, b, m0, seen, nullptr)) * mult;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sm.warp_total[warp] = incl;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += sm.warp_total[w];
+    total += sm.warp_total[w];
+  }
+  const long long blocks = max(1ll, min(static_cast<long long>(gridDim.x), (total + least - 1) / least));
+  const long long i = blockIdx.x;
+  const long long lo = i < blocks ? total * i / blocks : total;
+  const long long hi = i < blocks ? total * (i + 1) / blocks : total;
+  if (threadIdx.x == 0) {
+    sm.lo = lo;
+    sm.hi = hi;
+    sm.total = total;
+    sm.blocks = static_cast<int>(blocks);
+  }
+  long long at = before + incl - mine;
+  if (lo >= at && lo < at + mine) {
+    for (long long e = e0; e < e1; ++e) {
+      const long long n = static_cast<long long>(en.steps(e, b, m0, seen, nullptr)) * mult;
+      if (lo < at + n) {
+        sm.entry = static_cast<int>(e);
+        sm.rem = lo - at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+}
+
+// Block that holds position x of the line: the last i with total i / blocks <= x.
+__device__ __forceinline__ int piece_of(long long x, long long total, int blocks) {
+  return static_cast<int>(((x + 1) * blocks - 1) / total);
+}
+
+}  // namespace kv4
+}  // namespace fvattn

@@ -143,7 +143,7 @@ def _ws(workspace):
 
 def fvattn_kv4_workspace_bytes(op: int, cache: KV4Cache, batch: KV4Batch, rows: int, H_q: int = 0) -> int:
     """Workspace bytes of an FVATTN_OP_KV4_* call over ``rows`` rows with ``H_q`` query heads."""
-    c, b = cache._struct(), batch._struct(rows)
+    c, b = cache._struct(), batch._struct(rows)   # the attention's grows with the batch's max_q
     return int(_lib.fvattn_kv4_workspace_bytes(op, ctypes.byref(c), ctypes.byref(b), int(H_q)))
 
 
@@ -225,7 +225,7 @@ class KV4Path:
         if p is not None:
             self.kv_idx = torch.empty((max_rows, cache.H, max_pages), dtype=torch.int32, device=dev)
             self.kv_cnt = torch.empty((max_rows, cache.H), dtype=torch.int32, device=dev)
-        b = _BatchStruct(None, None, None, self.max_batch, self.max_pages, self.max_rows, 1)
+        b = _BatchStruct(None, None, None, self.max_batch, self.max_pages, self.max_rows, self.max_rows)
         c = cache._struct()
 
         def workspace(op):

@@ -446,7 +446,8 @@ typedef struct {
 
 /* Workspace bytes of the calls below: op = FVATTN_OP_KV4_*, Hq = query heads (a multiple of
  * the cache's H; ignored by append and read). Pointers in the structs are not looked at. 0
- * if the sizes are invalid. 256-byte aligned, status word first, as for the other calls.
+ * if the sizes are invalid. A workspace sized for a batch serves every batch that has no more
+ * sequences, pages, rows or max_q. 256-byte aligned, status word first, as for the other calls.
  * One workspace serves one call at a time: calls that overlap on the GPU (two streams, two
  * captured graphs replayed at once) need one each. */
 FVATTN_API size_t fvattn_kv4_workspace_bytes(fvattn_op op, const fvattn_kv4_cache* cache,
@@ -498,9 +499,11 @@ FVATTN_API fvattn_status fvattn_kv4_select(const fvattn_kv4_cache* cache, const 
  * the scaled logits (-inf for a row that sees none). Without lists kv_idx and kv_cnt are NULL.
  * Lists ascend strictly: an entry that is not above the one before it, or lies outside the
  * sequence's pages, is left out and recorded as FVATTN_ERR_INVALID_ARG.
+ * Calls with the same arguments give the same bits; where a row's sum is split depends on the
+ * lengths of the whole batch, so a row's rounding does too.
  * Stored values enter the products exactly (fp16 holds them); the softmax and all sums are fp32.
- * BF16: q enters exactly (scaled by a power of two; elements below 2^-24 of a row's largest round to
- * that grid), P is rounded to fp16. FP32: q and P are split into two fp16 parts each.
+ * BF16: q enters exactly (scaled by a power of two; elements below 2^-30 of a row's largest may lose
+ * bits below 2^-37 of it), P is rounded to fp16. FP32: q and P are split into two fp16 parts each.
  * scale > 0, Hq/H <= 64. */
 FVATTN_API fvattn_status fvattn_kv4_attn(const fvattn_kv4_cache* cache, const fvattn_kv4_batch* batch,
                                          const void* q, int64_t q_stride, int Hq, void* out, float* lse,
