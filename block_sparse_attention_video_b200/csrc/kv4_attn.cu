@@ -5,10 +5,10 @@
 // Units of up to 8 NT query rows, cut into equal pieces over the blocks (kv4_units.cuh).
 //
 // A block is one producer warp, which brings whole page records into a ring of shared
-// memory (one bulk copy a page, 18 KB at d 128), and eight consumer warps with 16 keys of
-// the step each. What bounds it is HBM: d + d/8 bytes of K and V a token and KV head.
+// memory (one bulk copy a page, 18 KB at d 128), and four consumer warps with 32 keys of
+// the step each, as two tiles of 16 whose chains of instructions overlap. What bounds it is HBM: d + d/8 bytes of K and V a token and KV head.
 //
-// Arithmetic per warp and step, on m16n8k16 fp16 products with fp32 sums:
+// Arithmetic per tile, on m16n8k16 fp16 products with fp32 sums:
 //   S^T [16 keys x 8 rows]     = K [16 x d] Q^T      K's codes become fp16 in registers
 //   O^T [16 channels x 8 rows] += V^T [16 x 16 keys] P^T
 // The transposed forms put keys (channels) on the 16-wide side and the few query rows on
@@ -32,16 +32,18 @@
 namespace fvattn {
 namespace kv4 {
 
-constexpr int kConsumers = 8;                       // consumer warps, 16 keys each
+constexpr int kConsumers = 4;                       // consumer warps
+constexpr int kTiles = 2;                           // tiles of 16 keys a warp and step
 constexpr int kThreads = (kConsumers + 1) * 32;
-static_assert(kStep == kConsumers * 16, "");
+constexpr int kLeast = 4;                           // steps a block takes at least: joining costs about as much
+static_assert(kStep == kConsumers * kTiles * 16, "");
 
 template <int HD, int NT>
 struct Shape {
   static constexpr int RT = 8 * NT;
   static constexpr int kStageBytes = kStep * (HD + HD / 8);
-  // about 92 KB of ring a block with two blocks on an SM (NT 1), 184 KB with one
-  static constexpr int kStages = (NT == 1 ? 5 : 10) * (128 / HD);
+  // three blocks on an SM with 55 KB of ring each; two with 74 KB beside the larger sums of NT 2
+  static constexpr int kStages = (NT == 1 ? 3 : 4) * (128 / HD);
   static constexpr int kPart = RT * HD + 2 * RT;    // floats of a partial result
 };
 
@@ -49,14 +51,17 @@ template <int HD, int NT>
 struct __align__(128) AttnSmem {
   using S = Shape<HD, NT>;
   uint8_t ring[S::kStages][S::kStageBytes];
-  float slab[4][S::RT][HD];
+  float slab[kConsumers][S::RT][HD];
   float mx[2][kConsumers][S::RT];
   float sum[2][kConsumers][S::RT];
-  Meta meta[S::kStages];
+  int4 step[S::kStages];  // first keys of the stage's two pages (-1: no such page), -, unit ends here
+  Meta unit[2];
+  uint64_t unit_full[2], unit_empty[2];
   uint64_t full[S::kStages];
   uint64_t empty[S::kStages];
   uint64_t sync;
   Piece piece;
+  Seqs seqs;
   int joiner;
   int abort_flag;
 };
@@ -88,127 +93,130 @@ __device__ __forceinline__ uint32_t e4m3x2(uint32_t two_codes) {
   const __half2 h = e4m3x2_to_half2(two_codes);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// Bounded wait of a whole warp; one poll and a vote when the phase is there already.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
+}
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(float x) { return x; }
 
-template <typename T, int HD, int NT>
+// The producer warp: walks the piece's units, publishes each before its pages, and keeps
+// the ring full.
+template <int HD, int NT>
 __device__ void produce(const AttnParams& P, AttnSmem<HD, NT>& sm) {
   using S = Shape<HD, NT>;
   constexpr int RT = S::RT;
   const int lane = threadIdx.x & 31;
   volatile int* abort_flag = &sm.abort_flag;
-  const Entries<RT> en{P};
+  const Entries<RT> en(P, sm.seqs);
   const long long E = en.count();
   const int mult = en.times();
   const int per = kStep / P.block;                 // pages per step
   const int rec = Layout(HD, P.block).rec;
   const long long total = sm.piece.total, lo = sm.piece.lo, hi = sm.piece.hi;
-  long long entry = sm.piece.entry, rem = sm.piece.rem;
+  long long entry = sm.piece.entry;
   Meta m;
-  int b = 0, m0 = 0, seen = 0, steps = 0, s = 0, which = 0, cnt = 0, it = 0;
-  int window = -1, w_page = 0, w_slot = -1;        // 32 page positions of the unit, one a lane
-  bool fresh = true, ok = true;
-  for (long long x = lo; x < hi; ++x, ++it) {
-    bool first = false;
-    if (fresh) {                                   // the unit at position x
-      if (x == lo) {
-        steps = max(1, en.steps(entry, b, m0, seen, &m));
-        which = static_cast<int>(rem / steps);
-        s = static_cast<int>(rem - static_cast<long long>(which) * steps);
-      } else {
-        s = 0;
-        if (++which == mult) {
-          which = 0;
-          do ++entry; while (entry < E && en.steps(entry, b, m0, seen, nullptr) == 0);
-          if (entry >= E) {                        // lengths changed under the kernel
-            ok = false;
-            break;
-          }
-        }
-        steps = max(1, en.steps(entry, b, m0, seen, &m));
+  int b = 0, m0 = 0, seen = 0, steps = 0, which = 0, it = 0, un = 0;
+  bool ok = true;
+  for (long long x = lo; ok && x < hi; x += m.ns) {
+    m.s0 = 0;
+    if (x == lo) {
+      steps = max(1, en.steps(entry, b, m0, seen, &m));
+      which = static_cast<int>(sm.piece.rem / steps);
+      m.s0 = static_cast<int>(sm.piece.rem - static_cast<long long>(which) * steps);
+    } else if (++which == mult) {
+      which = 0;
+      do ++entry; while (entry < E && (steps = en.steps(entry, b, m0, seen, &m)) == 0);
+      if (entry >= E) {                            // lengths changed under the kernel
+        ok = false;
+        break;
       }
-      if (P.kv_idx) {
-        m.h = static_cast<int>(entry % P.c.H);
-        m.m0 = m0 + which * RT;
-        m.mc = min(RT, P.G - which * RT);
-        cnt = min(max(__ldg(P.kv_cnt + entry), 0), P.bt.max_pages);
-      } else {
-        m.h = which;
-        m.m0 = m0;
-        m.mc = static_cast<int>(min(static_cast<long long>(RT),
-                                    static_cast<long long>(min(m.q, P.bt.rows - m.cu)) * P.G - m0));
-        cnt = (seen + P.block - 1) / P.block;
-      }
-      m.seen = seen;
-      m.begin = piece_of(x - s, total, sm.piece.blocks);
-      m.end = piece_of(x - s + steps - 1, total, sm.piece.blocks);
-      window = -1;
-      first = true;
-      fresh = false;
     }
-    int slot[2] = {-1, -1};
-    m.key0[0] = m.key0[1] = -1;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (k >= per) break;
-      const int pos = s * per + k;
-      if (pos >= cnt) break;
+    int cnt;                                       // pages of the unit
+    if (P.kv_idx) {
+      m.h = static_cast<int>(entry % P.c.H);
+      m.m0 = m0 + which * RT;
+      m.mc = min(RT, P.G - which * RT);
+      cnt = min(max(__ldg(P.kv_cnt + entry), 0), P.bt.max_pages);
+    } else {
+      m.h = which;
+      m.m0 = m0;
+      m.mc = static_cast<int>(
+          min(static_cast<long long>(RT), static_cast<long long>(min(m.q, P.bt.rows - m.cu)) * P.G - m0));
+      cnt = (seen + P.block - 1) / P.block;
+    }
+    m.seen = seen;
+    m.ns = static_cast<int>(min(static_cast<long long>(steps - m.s0), hi - x));
+    m.begin = piece_of(x - m.s0, total, sm.piece.blocks);
+    m.end = piece_of(x - m.s0 + steps - 1, total, sm.piece.blocks);
+    // Pool slots of 32 pages of the unit at a time, one a lane, and the first key of each.
+    int window = (m.s0 * per) >> 5, w_slot = -1, w_key = -1;
+    auto look_up = [&]() {
+      const int p = window * 32 + lane;
+      w_slot = w_key = -1;
+      if (p >= cnt) return;
+      int page = p;
+      if (P.kv_idx) {
+        const int* list = P.kv_idx + entry * P.bt.max_pages;
+        page = __ldg(list + p);
+        const int before = p ? __ldg(list + p - 1) : -1;
+        if (page < 0 || static_cast<long long>(page) * P.block >= m.n || (p && page <= before)) {
+          record_status(P.status, FVATTN_ERR_INVALID_ARG);
+          return;
+        }
+        if (page * P.block >= seen) return;
+      }
+      w_slot = pool_slot(P.bt, P.c.num_pages, b, page, P.status);
+      if (w_slot >= 0) w_key = page * P.block;
+    };
+    const int u = un & 1;
+    if (!warp_wait(&sm.unit_empty[u], ((un >> 1) & 1) ^ 1, abort_flag, P.status)) { ok = false; break; }
+    ++un;
+    if (lane == 0) {
+      sm.unit[u] = m;
+      mbar_arrive(&sm.unit_full[u]);
+    }
+    look_up();
+    const uint8_t* pool = P.c.pages + static_cast<size_t>(m.h) * rec;
+    const size_t slot_bytes = static_cast<size_t>(P.c.H) * rec;
+    for (int s = m.s0; s < m.s0 + m.ns; ++s, ++it) {
+      const int pos = s * per;                     // the pages of a step share a window
       if ((pos >> 5) != window) {
         window = pos >> 5;
-        const int p = window * 32 + lane;
-        w_page = p;
-        w_slot = -1;
-        if (p < cnt) {
-          bool good = true;
-          if (P.kv_idx) {
-            const int* list = P.kv_idx + entry * P.bt.max_pages;
-            w_page = __ldg(list + p);
-            good = w_page >= 0 && static_cast<long long>(w_page) * P.block < m.n && (p == 0 || w_page > __ldg(list + p - 1));
-            if (!good) record_status(P.status, FVATTN_ERR_INVALID_ARG);
-            good = good && w_page * P.block < seen;
-          }
-          if (good) w_slot = pool_slot(P.bt, P.c.num_pages, b, w_page, P.status);
-        }
+        look_up();
       }
-      slot[k] = __shfl_sync(0xffffffffu, w_slot, pos & 31);
-      const int page = __shfl_sync(0xffffffffu, w_page, pos & 31);
-      if (slot[k] >= 0) m.key0[k] = page * P.block;
+      const int slot0 = __shfl_sync(0xffffffffu, w_slot, pos & 31), key0 = __shfl_sync(0xffffffffu, w_key, pos & 31);
+      int slot1 = __shfl_sync(0xffffffffu, w_slot, (pos + 1) & 31), key1 = __shfl_sync(0xffffffffu, w_key, (pos + 1) & 31);
+      if (per == 1) slot1 = key1 = -1;
+      const int st = it % S::kStages;
+      if (!warp_wait(&sm.empty[st], ((it / S::kStages) & 1) ^ 1, abort_flag, P.status)) { ok = false; break; }
+      if (lane == 0) {
+        sm.step[st] = make_int4(key0, key1, 0, s + 1 == m.s0 + m.ns);
+        const uint32_t bytes = ((slot0 >= 0) + (slot1 >= 0)) * rec;
+        if (bytes) mbar_arrive_expect_tx(&sm.full[st], bytes); else mbar_arrive(&sm.full[st]);
+        if (slot0 >= 0) bulk_load(sm.ring[st], pool + slot0 * slot_bytes, rec, &sm.full[st]);
+        if (slot1 >= 0) bulk_load(sm.ring[st] + rec, pool + slot1 * slot_bytes, rec, &sm.full[st]);
+      }
+      __syncwarp();
     }
-    m.first = first;
-    m.last = s + 1 == steps || x + 1 == hi;
-    const int st = it % S::kStages;
-    if (!__all_sync(0xffffffffu, mbar_wait(&sm.empty[st], ((it / S::kStages) & 1) ^ 1, abort_flag, P.status))) {
-      ok = false;
-      break;
-    }
-    if (lane == 0) {
-      sm.meta[st] = m;
-      const uint32_t bytes = ((slot[0] >= 0) + (slot[1] >= 0)) * rec;
-      if (bytes) mbar_arrive_expect_tx(&sm.full[st], bytes); else mbar_arrive(&sm.full[st]);
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (slot[k] >= 0)
-          bulk_load(sm.ring[st] + k * rec, P.c.pages + (static_cast<size_t>(slot[k]) * P.c.H + m.h) * rec, rec,
-                    &sm.full[st]);
-    }
-    __syncwarp();
-    if (++s == steps) fresh = true;
   }
   // every copy has landed before the block may end
-  if (!ok || hi > lo)
-    for (int o = max(0, it - S::kStages); o < it; ++o) mbar_wait_plain(&sm.full[o % S::kStages], (o / S::kStages) & 1);
+  for (int o = max(0, it - S::kStages); o < it; ++o) mbar_wait_plain(&sm.full[o % S::kStages], (o / S::kStages) & 1);
 }
 
 template <typename T, int HD, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_stream_kernel(const AttnParams P) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : sizeof(T) == 4 ? 1 : 2)
+    attn_stream_kernel(const AttnParams P) {
   using S = Shape<HD, NT>;
   constexpr int RT = S::RT;
   constexpr bool kExact = sizeof(T) == 4;          // fp32: operands in two fp16 parts
   constexpr int KS = HD / 16;                      // k-steps of S, and 16-channel tiles of O
   constexpr int KW = HD / 32;                      // 32-bit words of K a lane and key
-  extern __shared__ uint8_t smem_raw[];
-  AttnSmem<HD, NT>& sm =
-      *reinterpret_cast<AttnSmem<HD, NT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
+  // 16-byte alignment is all that the copies need; the struct sits at the start as it is, so
+  // that every access is known to be to shared memory
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  AttnSmem<HD, NT>& sm = *reinterpret_cast<AttnSmem<HD, NT>*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &sm.abort_flag;
   if (threadIdx.x == 0) {
@@ -216,16 +224,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_stream_kernel(
       mbar_init(&sm.full[i], 1);
       mbar_init(&sm.empty[i], kConsumers);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.unit_full[i], 1);
+      mbar_init(&sm.unit_empty[i], kConsumers);
+    }
     mbar_init(&sm.sync, kConsumers);
     sm.abort_flag = 0;
     fence_mbarrier_init();
-    if (blockIdx.x == 0 && __ldg(P.bt.cu + P.bt.B) > P.bt.rows) record_status(P.status, FVATTN_ERR_INVALID_ARG);
   }
-  find_piece<RT, kThreads>(P, sm.piece, 2);        // a block's own costs are about one step's
+  find_piece<RT, kThreads>(P, sm.seqs, sm.piece, kLeast);
   const int len = static_cast<int>(sm.piece.hi - sm.piece.lo);
   if (len <= 0) return;
   if (warp == kConsumers) {
-    produce<T, HD, NT>(P, sm);
+    produce<HD, NT>(P, sm);
+    if (blockIdx.x == 0 && (threadIdx.x & 31) == 0 && __ldg(P.bt.cu + P.bt.B) > P.bt.rows)
+      record_status(P.status, FVATTN_ERR_INVALID_ARG);
     return;
   }
 
@@ -236,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_stream_kernel(
   auto meet = [&]() -> bool {
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.sync);
-    return __all_sync(0xffffffffu, mbar_wait(&sm.sync, met++ & 1, abort_flag, P.status));
+    return warp_wait(&sm.sync, met++ & 1, abort_flag, P.status);
   };
   const int g = lane >> 2, t = lane & 3;
   // Row g of a tile is the tile's key g ^ (g>>1 & 1): neighbouring lanes' V rows then lie
@@ -244,19 +257,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_stream_kernel(
   const int gk = g ^ ((g >> 1) & 1);
   const int ka = (2 * t) ^ (t & 1), kb = (2 * t + 1) ^ (t & 1);
   const Layout L(HD, P.block);
-  const int pg = warp * 16 / P.block;              // page of the stage that holds the warp's keys
-  const int k_in = warp * 16 - pg * P.block;       // first of them inside the page
+  const int pg = warp * (16 * kTiles) / P.block;   // page of the stage that holds the warp's keys
+  const int k_in = warp * (16 * kTiles) - pg * P.block;   // first of them inside the page
   uint32_t qh[NT][KS][2], ql[kExact ? NT : 1][kExact ? KS : 1][2];
   float o[NT][KS][4], mref[NT][2], l[NT][2], cs[NT][2];
-  int see[NT][2], unit_par = 0, all_seen = 0;
+  int see[NT][2], all_seen = 0;
+  bool fresh = true;
+  int units = 0;
   for (int it = 0; it < len; ++it) {
     const int st = it % S::kStages;
-    if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[st], (it / S::kStages) & 1, abort_flag, P.status))) return;
-    const Meta& m = sm.meta[st];
-    if (m.first) {
+    const Meta& m = sm.unit[units & 1];
+    if (fresh) {                                   // Q comes while the first pages are on their way
+      if (!warp_wait(&sm.unit_full[units & 1], (units >> 1) & 1, abort_flag, P.status)) return;
+      fresh = false;
       const int mc = m.mc, m0 = m.m0, h = m.h, cu = m.cu, nq = m.q, n = m.n;
       const float base = P.scale_log2 * (P.c.k_scale ? __ldg(P.c.k_scale + h) : 1.f);
-      all_seen = n;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const int rr = j * 8 + g;                  // this lane's Q row
@@ -316,100 +331,89 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_stream_kernel(
       }
       all_seen = m.seen;
     }
-    const int key0 = pg < 2 ? m.key0[pg] : -1;
+    if (!warp_wait(&sm.full[st], (it / S::kStages) & 1, abort_flag, P.status)) return;
+    const int4 now = sm.step[st];
+    const int key0 = pg == 0 ? now.x : now.y;
     const int kbase = key0 + k_in;                 // the warp's first key of the sequence
     if (key0 >= 0 && kbase < all_seen) {           // warp-uniform
       const uint8_t* rp = sm.ring[st] + pg * L.rec;
       // ---- S^T
-      uint32_t kw[2][KW], ksc[2][2];               // K words and scales of the two keys
+      float s[kTiles][NT][4];
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int key = k_in + gk + 8 * y;
-        const uint8_t* p = rp + key * (HD / 2) + t * (HD / 8);
-        if constexpr (HD == 128) {
-          const uint4 w = *reinterpret_cast<const uint4*>(p);
-          kw[y][0] = w.x; kw[y][1] = w.y; kw[y][2] = w.z; kw[y][3] = w.w;
-          const uint32_t sc = e4m3x2(*reinterpret_cast<const uint16_t*>(rp + L.kscale() + key * 8 + 2 * t));
-          ksc[y][0] = __byte_perm(sc, 0, 0x1010);
-          ksc[y][1] = __byte_perm(sc, 0, 0x3232);
-        } else {
-          const uint2 w = *reinterpret_cast<const uint2*>(p);
-          kw[y][0] = w.x; kw[y][1] = w.y;
-          const uint32_t sc = rp[L.kscale() + key * 4 + t];
-          ksc[y][0] = ksc[y][1] = e4m3x2(sc | (sc << 8));
-        }
-      }
-      float s[NT][4];
-#pragma unroll
-      for (int j = 0; j < NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-#pragma unroll
-      for (int w = 0; w < KW; ++w) {
-        uint32_t x[2][4];
+      for (int u = 0; u < kTiles; ++u) {
+        uint32_t kw[2][KW], ksc[2][2];             // K words and scales of two keys
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          e2m1x8_to_half2(kw[y][w], x[y]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[y][i] = mul2(x[y][i], ksc[y][HD == 128 ? w / 2 : 0]);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t a[4] = {x[0][2 * i], x[1][2 * i], x[0][2 * i + 1], x[1][2 * i + 1]};
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            mma_f16(s[j], a, qh[j][2 * w + i][0], qh[j][2 * w + i][1]);
-            if constexpr (kExact) mma_f16(s[j], a, ql[j][2 * w + i][0], ql[j][2 * w + i][1]);
-          }
-        }
-      }
-      // ---- V words of keys ka, kb and ka + 8, kb + 8, and their scales
-      constexpr int VW = HD / 64;                  // 32-bit words of a lane's HD/8 channels
-      uint32_t vw[4][VW], vsc[2];
-      {
-        uint32_t b[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int key = k_in + ((y & 1) ? kb : ka) + 8 * (y >> 1);
-          const uint8_t* p = rp + L.vcodes() + key * (HD / 2) + g * (HD / 16);
+          const int key = k_in + 16 * u + gk + 8 * y;
+          const uint8_t* p = rp + key * (HD / 2) + t * (HD / 8);
           if constexpr (HD == 128) {
-            const uint2 w = *reinterpret_cast<const uint2*>(p);
-            vw[y][0] = w.x; vw[y][1] = w.y;
-            b[y] = rp[L.vscale() + key * 8 + g];
+            const uint4 w = *reinterpret_cast<const uint4*>(p);
+            kw[y][0] = w.x; kw[y][1] = w.y; kw[y][2] = w.z; kw[y][3] = w.w;
+            const uint32_t sc = e4m3x2(*reinterpret_cast<const uint16_t*>(rp + L.kscale() + key * 8 + 2 * t));
+            ksc[y][0] = __byte_perm(sc, 0, 0x1010);
+            ksc[y][1] = __byte_perm(sc, 0, 0x3232);
           } else {
-            vw[y][0] = *reinterpret_cast<const uint32_t*>(p);
-            b[y] = rp[L.vscale() + key * 4 + (g >> 1)];
+            const uint2 w = *reinterpret_cast<const uint2*>(p);
+            kw[y][0] = w.x; kw[y][1] = w.y;
+            const uint32_t sc = rp[L.kscale() + key * 4 + t];
+            ksc[y][0] = ksc[y][1] = e4m3x2(sc | (sc << 8));
           }
-          // behind the last key that a row sees the page holds anything, NaN scales too
-          if (kbase + key - k_in >= all_seen) b[y] = 0;
         }
-        vsc[0] = e4m3x2(b[0] | (b[1] << 8));
-        vsc[1] = e4m3x2(b[2] | (b[3] << 8));
+#pragma unroll
+        for (int j = 0; j < NT; ++j) s[u][j][0] = s[u][j][1] = s[u][j][2] = s[u][j][3] = 0.f;
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          uint32_t x[2][4];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            e2m1x8_to_half2(kw[y][w], x[y]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[y][i] = mul2(x[y][i], ksc[y][HD == 128 ? w / 2 : 0]);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t a[4] = {x[0][2 * i], x[1][2 * i], x[0][2 * i + 1], x[1][2 * i + 1]};
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              mma_f16(s[u][j], a, qh[j][2 * w + i][0], qh[j][2 * w + i][1]);
+              if constexpr (kExact) mma_f16(s[u][j], a, ql[j][2 * w + i][0], ql[j][2 * w + i][1]);
+            }
+          }
+        }
       }
-      // ---- softmax: base-2 logits of keys gk, gk + 8 for rows 2t, 2t + 1 of each tile
-      uint32_t ph[NT][2], pl[NT][2];
+      // ---- softmax: base-2 logits of keys gk, gk + 8 of each tile for rows 2t, 2t + 1
+      constexpr int kSpan = 16 * kTiles;
+      uint32_t ph[kTiles][NT][2], pl[kExact ? kTiles : 1][NT][2];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
+        if (kbase + kSpan > min(see[j][0], see[j][1])) {   // some key is behind a row's last
+#pragma unroll
+          for (int u = 0; u < kTiles; ++u)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              if (kbase + 16 * u + gk + 8 * (y >> 1) >= see[j][y & 1]) s[u][j][y] = -INFINITY;
+        }
+        float x[2];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          if (kbase + 15 >= see[j][y]) {           // some key is behind the row's last
-            if (kbase + gk >= see[j][y]) s[j][y] = -INFINITY;
-            if (kbase + gk + 8 >= see[j][y]) s[j][2 + y] = -INFINITY;
-          }
+          float mx = fmaxf(s[0][j][y], s[0][j][2 + y]);
+#pragma unroll
+          for (int u = 1; u < kTiles; ++u) mx = fmax3(mx, s[u][j][y], s[u][j][2 + y]);
+          x[y] = mx * cs[j][y];
         }
-        const float x0 = fmaxf(s[j][0], s[j][2]) * cs[j][0], x1 = fmaxf(s[j][1], s[j][3]) * cs[j][1];
         // The max only has to be near: raised, for all keys of the warp, when it is
         // exceeded by 2^8.
-        const bool raise = x0 > mref[j][0] + (kHead + kRaise) || x1 > mref[j][1] + (kHead + kRaise);
+        const bool raise = x[0] > mref[j][0] + (kHead + kRaise) || x[1] > mref[j][1] + (kHead + kRaise);
         if (__any_sync(0xffffffffu, raise)) {
-          float mx[2] = {x0, x1};
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) {
-            mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], d));
-            mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], d));
+            x[0] = fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], d));
+            x[1] = fmaxf(x[1], __shfl_xor_sync(0xffffffffu, x[1], d));
           }
           float f[2];
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const float nm = fmaxf(mref[j][y], mx[y] - kHead);
+            const float nm = fmaxf(mref[j][y], x[y] - kHead);
             f[y] = ex2_approx(mref[j][y] - nm);
             mref[j][y] = nm;
             l[j][y] *= f[y];
@@ -422,52 +426,81 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_stream_kernel(
             o[j][i][3] *= f[1];
           }
         }
-        float p[4];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) p[y] = ex2_approx(fmaf(s[j][y], cs[j][y & 1], -mref[j][y & 1]));
-        l[j][0] += p[0] + p[2];
-        l[j][1] += p[1] + p[3];
-        const uint32_t h0 = pack2(p[0], p[1]), h1 = pack2(p[2], p[3]);
-        ph[j][0] = transpose8x8(h0);
-        ph[j][1] = transpose8x8(h1);
-        if constexpr (kExact) {
-          const float2 r0 = unpack2(h0), r1 = unpack2(h1);
-          pl[j][0] = transpose8x8(pack2(p[0] - r0.x, p[1] - r0.y));
-          pl[j][1] = transpose8x8(pack2(p[2] - r1.x, p[3] - r1.y));
+        for (int u = 0; u < kTiles; ++u) {
+          float p[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) p[y] = ex2_approx(fmaf(s[u][j][y], cs[j][y & 1], -mref[j][y & 1]));
+          l[j][0] += p[0] + p[2];
+          l[j][1] += p[1] + p[3];
+          const uint32_t h0 = pack2(p[0], p[1]), h1 = pack2(p[2], p[3]);
+          ph[u][j][0] = transpose8x8(h0);
+          ph[u][j][1] = transpose8x8(h1);
+          if constexpr (kExact) {
+            const float2 r0 = unpack2(h0), r1 = unpack2(h1);
+            pl[u][j][0] = transpose8x8(pack2(p[0] - r0.x, p[1] - r0.y));
+            pl[u][j][1] = transpose8x8(pack2(p[2] - r1.x, p[3] - r1.y));
+          }
         }
       }
-      // ---- O^T
+      // ---- O^T: V words of keys ka, kb and ka + 8, kb + 8 of each tile, and their scales
+      constexpr int VW = HD / 64;                  // 32-bit words of a lane's HD/8 channels
+      const bool edge = kbase + kSpan > all_seen;
 #pragma unroll
-      for (int w = 0; w < VW; ++w) {
-        // two keys' codes of one channel side by side: the even channels, the odd ones
-        uint32_t x[4][4];
+      for (int u = 0; u < kTiles; ++u) {
+        uint32_t vw[4][VW], b[4], vsc[2];
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const uint32_t a = vw[2 * y][w], b = vw[2 * y + 1][w];
-          e2m1x8_to_half2((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), x[2 * y]);
-          e2m1x8_to_half2(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), x[2 * y + 1]);
+        for (int y = 0; y < 4; ++y) {
+          const int key = k_in + 16 * u + ((y & 1) ? kb : ka) + 8 * (y >> 1);
+          const uint8_t* p = rp + L.vcodes() + key * (HD / 2) + g * (HD / 16);
+          if constexpr (HD == 128) {
+            const uint2 w = *reinterpret_cast<const uint2*>(p);
+            vw[y][0] = w.x; vw[y][1] = w.y;
+            b[y] = rp[L.vscale() + key * 8 + g];
+          } else {
+            vw[y][0] = *reinterpret_cast<const uint32_t*>(p);
+            b[y] = rp[L.vscale() + key * 4 + (g >> 1)];
+          }
         }
+        if (edge) {
+          // behind the last key that a row sees the page holds anything, NaN scales too
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t a[4] = {mul2(x[0][i], vsc[0]), mul2(x[1][i], vsc[0]), mul2(x[2][i], vsc[1]),
-                                 mul2(x[3][i], vsc[1])};
+          for (int y = 0; y < 4; ++y)
+            if (kbase + 16 * u + ((y & 1) ? kb : ka) + 8 * (y >> 1) >= all_seen) b[y] = 0;
+        }
+        vsc[0] = e4m3x2(b[0] | (b[1] << 8));
+        vsc[1] = e4m3x2(b[2] | (b[3] << 8));
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            if constexpr (kExact) {
-              float d[4] = {0.f, 0.f, 0.f, 0.f};
-              mma_f16(d, a, pl[j][0], pl[j][1]);
-              mma_f16(d, a, ph[j][0], ph[j][1]);
+        for (int w = 0; w < VW; ++w) {
+          // two keys' codes of one channel side by side: the even channels, the odd ones
+          uint32_t x[4][4];
 #pragma unroll
-              for (int y = 0; y < 4; ++y) o[j][4 * w + i][y] += d[y];
-            } else {
-              mma_f16(o[j][4 * w + i], a, ph[j][0], ph[j][1]);
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t c0 = vw[2 * y][w], c1 = vw[2 * y + 1][w];
+            e2m1x8_to_half2((c0 & 0x0F0F0F0Fu) | ((c1 << 4) & 0xF0F0F0F0u), x[2 * y]);
+            e2m1x8_to_half2(((c0 >> 4) & 0x0F0F0F0Fu) | (c1 & 0xF0F0F0F0u), x[2 * y + 1]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a[4] = {mul2(x[0][i], vsc[0]), mul2(x[1][i], vsc[0]), mul2(x[2][i], vsc[1]),
+                                   mul2(x[3][i], vsc[1])};
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              if constexpr (kExact) {
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_f16(d, a, pl[u][j][0], pl[u][j][1]);
+                mma_f16(d, a, ph[u][j][0], ph[u][j][1]);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) o[j][4 * w + i][y] += d[y];
+              } else {
+                mma_f16(o[j][4 * w + i], a, ph[u][j][0], ph[u][j][1]);
+              }
             }
           }
         }
       }
     }
-    const bool last = m.last;
-    if (!last) {
+    if (!now.w) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.empty[st]);
       continue;
@@ -475,8 +508,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_stream_kernel(
     // ------------------------------------------------------------ end of the unit's piece
     const int mc = m.mc, m0 = m.m0, h = m.h, cu = m.cu, begin = m.begin, end = m.end;
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.empty[st]);
-    const int par = unit_par++ & 1;
+    if (lane == 0) {
+      mbar_arrive(&sm.empty[st]);
+      mbar_arrive(&sm.unit_empty[units & 1]);
+    }
+    fresh = true;
+    const int par = units++ & 1;
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -508,23 +545,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_stream_kernel(
           for (int y = 0; y < 2; ++y)
             fn(j * 8 + 2 * t + y, g * (HD / 8) + 2 * i, o[j][i][y], o[j][i][2 + y], f[j][y]);
     };
-    if (warp >= 4)
-      each([&](int row, int ch, float a, float b, float fac) {
-        *reinterpret_cast<float2*>(&sm.slab[warp - 4][row][ch]) = make_float2(a * fac, b * fac);
-      });
-    if (!meet()) return;
-    if (warp < 4)
-      each([&](int row, int ch, float a, float b, float fac) {
-        float2* p = reinterpret_cast<float2*>(&sm.slab[warp][row][ch]);
-        const float2 v = *p;
-        *p = make_float2(fmaf(a, fac, v.x), fmaf(b, fac, v.y));
-      });
+    each([&](int row, int ch, float a, float b, float fac) {
+      *reinterpret_cast<float2*>(&sm.slab[warp][row][ch]) = make_float2(a * fac, b * fac);
+    });
     if (!meet()) return;
     const bool whole = begin == end;
     float* mine = P.part + (static_cast<size_t>(blockIdx.x) * 2 + (begin == static_cast<int>(blockIdx.x) ? 1 : 0)) * S::kPart;
     const float vs = P.c.v_scale ? __ldg(P.c.v_scale + h) : 1.f;
     constexpr int kPer = RT * HD / 4 / (kConsumers * 32);   // float4 a thread
-    static_assert(RT * HD / 4 % (kConsumers * 32) == 0 || RT * HD / 4 < kConsumers * 32, "");
+    static_assert(RT * HD / 4 % (kConsumers * 32) == 0, "");
     auto finish = [&](int row, int ch, float4 v, float mx, float sum) {
       if (row >= mc) return;
       const int i = (m0 + row) / P.G, gg = (m0 + row) - i * P.G;
@@ -539,9 +568,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_stream_kernel(
       if (P.lse && ch == 0) P.lse[at] = sum > 0.f || sum != sum ? (mx + log2f(sum)) * kLn2 : -INFINITY;
     };
 #pragma unroll
-    for (int k = 0; k < (kPer > 0 ? kPer : 1); ++k) {
+    for (int k = 0; k < kPer; ++k) {
       const int at = (threadIdx.x + k * kConsumers * 32) * 4;
-      if (at >= RT * HD) break;
       const int row = at / HD, ch = at % HD;
       float mx = kFloor;
       for (int w = 0; w < kConsumers; ++w) mx = fmaxf(mx, sm.mx[par][w][row]);
@@ -549,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_stream_kernel(
       for (int w = 0; w < kConsumers; ++w) sum += sm.sum[par][w][row] * ex2_approx(sm.mx[par][w][row] - mx);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
+      for (int w = 0; w < kConsumers; ++w) {
         const float4 a = *reinterpret_cast<const float4*>(&sm.slab[w][row][ch]);
         v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
       }
@@ -578,9 +606,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_stream_kernel(
       return P.part + (static_cast<size_t>(i) * 2 + (i == begin ? 1 : 0)) * S::kPart;
     };
 #pragma unroll
-    for (int k = 0; k < (kPer > 0 ? kPer : 1); ++k) {
+    for (int k = 0; k < kPer; ++k) {
       const int at = (threadIdx.x + k * kConsumers * 32) * 4;
-      if (at >= RT * HD) break;
       const int row = at / HD, ch = at % HD;
       if (row >= mc) continue;
       float mx = kFloor;
@@ -602,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_stream_kernel(
 }
 
 // Workspace behind the header: arrival counters, then partial results.
-constexpr int kMaxBlocks = 320;                    // two blocks on each of 148 SMs, and room
+constexpr int kMaxBlocks = 448;                    // three blocks on each of 148 SMs
 constexpr int kMaxChunkBlocks = 160;
 
 size_t chunk_part_bytes(int d, int grid);
@@ -612,7 +639,7 @@ cudaError_t launch_chunk(const AttnParams& P, int d, int grid, cudaStream_t st);
 static bool many_rows(int max_q, int G) { return static_cast<long long>(max_q) * G > 16; }
 
 // Bytes behind the header that a call clears.
-size_t attn_ws_clear() { return kMaxBlocks * sizeof(int); }
+size_t attn_ws_clear() { return align_up(kMaxBlocks * sizeof(int), 256); }
 size_t attn_ws_bytes(int d, int max_q, int G) {
   const size_t few = static_cast<size_t>(kMaxBlocks) * 2 * (16 * d + 32) * sizeof(float);
   const size_t part = many_rows(max_q, G) ? max(few, chunk_part_bytes(d, kMaxChunkBlocks)) : few;
@@ -621,10 +648,10 @@ size_t attn_ws_bytes(int d, int max_q, int G) {
 
 template <typename T, int HD, int NT>
 static cudaError_t launch_stream(const AttnParams& P, int num_sms, cudaStream_t st) {
-  const int smem = static_cast<int>(sizeof(AttnSmem<HD, NT>)) + 128;
+  const int smem = static_cast<int>(sizeof(AttnSmem<HD, NT>));
   cudaError_t e = cudaFuncSetAttribute(attn_stream_kernel<T, HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int grid = min(kMaxBlocks, num_sms * (NT == 1 ? 2 : 1));
+  const int grid = min(kMaxBlocks, num_sms * (NT == 1 ? 3 : 2));
   attn_stream_kernel<T, HD, NT><<<grid, kThreads, smem, st>>>(P);
   return cudaGetLastError();
 }
@@ -649,7 +676,7 @@ cudaError_t launch_attn(const Cache& c, const Batch& bt, const void* q, long lon
   P.arrived = reinterpret_cast<int*>(ws);
   P.part = reinterpret_cast<float*>(ws + attn_ws_clear());
   if (bf16 && !kv_idx && many_rows(max_q, P.G)) return launch_chunk(P, d, min(kMaxChunkBlocks, num_sms), st);
-  // Eight query rows a unit leave two blocks on an SM; more rows than that take sixteen.
+  // Up to eight query rows a unit, or sixteen.
   const bool few = (kv_idx ? P.G : static_cast<long long>(max_q) * P.G) <= 8;
 #define FVATTN_KV4(T, HD) (few ? launch_stream<T, HD, 1>(P, num_sms, st) : launch_stream<T, HD, 2>(P, num_sms, st))
   if (bf16) return d == 128 ? FVATTN_KV4(__nv_bfloat16, 128) : FVATTN_KV4(__nv_bfloat16, 64);

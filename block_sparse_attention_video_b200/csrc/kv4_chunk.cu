@@ -70,6 +70,7 @@ struct __align__(1024) Smem {
   uint64_t meet[2];
   uint64_t mma_done;
   Piece piece;
+  Seqs seqs;
   int flags[kFlags];      // bit k: page k of the step is absent
   int joiner[2];
   uint32_t tmem_base;
@@ -91,7 +92,7 @@ template <int HD>
 __device__ void produce(const AttnParams& P, Smem<HD>& sm) {
   const int lane = threadIdx.x & 31;
   volatile int* abort_flag = &sm.abort_flag;
-  const Entries<kRows> en{P};
+  const Entries<kRows> en(P, sm.seqs);
   const int mult = en.times();
   const int per = kStep / P.block;
   const Layout L(HD, P.block);
@@ -605,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const AttnParam
     if (blockIdx.x == 0 && __ldg(P.bt.cu + P.bt.B) > P.bt.rows) record_status(P.status, FVATTN_ERR_INVALID_ARG);
   }
   // A unit's own costs (Q, epilogue) are about three steps'.
-  find_piece<kRows, kThreads>(P, sm.piece, 4);
+  find_piece<kRows, kThreads>(P, sm.seqs, sm.piece, 4);
   if (sm.piece.hi <= sm.piece.lo) return;    // block-uniform, nothing allocated yet
   if (warp == 8) {                           // whole warp
     tmem_alloc(&sm.tmem_base, 512);

@@ -37,9 +37,7 @@ struct AttnParams {
 };
 
 // A unit, as its producer publishes it to the other warps.
-struct Meta {
-  int key0[2];            // first key of the step's pages; -1: no such page
-  int first, last;        // first / last step of the unit in this block
+struct alignas(16) Meta {
   int cu, q, n;           // the sequence: first row, rows, tokens held
   int m0, mc;             // first (row, head) pair and their number
   int h;                  // KV head
@@ -49,6 +47,22 @@ struct Meta {
   int pad;
 };
 
+// First rows and lengths of the sequences, copied to shared memory where they are few: the
+// searches below are chains of loads.
+struct Seqs {
+  static constexpr int kMax = 256;
+  int cu[kMax + 1];
+  int kv_len[kMax];
+  template <int kThreads>
+  __device__ void load(const Batch& bt) {
+    if (bt.B > kMax) return;
+    for (int i = threadIdx.x; i <= bt.B; i += kThreads) {
+      cu[i] = __ldg(bt.cu + i);
+      if (i < bt.B) kv_len[i] = __ldg(bt.kv_len + i);
+    }
+  }
+};
+
 // Entries are what the units are counted by: without lists, tiles of RT pairs of a
 // sequence (each counts for all KV heads); with lists, (row, KV head) (each counts for
 // all tiles of its query heads). Tiles are numbered without a prefix sum: sequence b owns
@@ -56,49 +70,66 @@ struct Meta {
 template <int RT>
 struct Entries {
   const AttnParams& P;
+  const int* cu;          // shared memory or global
+  const int* kv_len;
+  __device__ Entries(const AttnParams& p, const Seqs& s)
+      : P(p), cu(p.bt.B <= Seqs::kMax ? s.cu : p.bt.cu), kv_len(p.bt.B <= Seqs::kMax ? s.kv_len : p.bt.kv_len) {}
   __device__ long long count() const {
     return P.kv_idx ? static_cast<long long>(P.bt.rows) * P.c.H
                     : static_cast<long long>(P.bt.rows) * P.G / RT + P.bt.B;
   }
   __device__ int times() const { return P.kv_idx ? (P.G + RT - 1) / RT : P.c.H; }
+  __device__ int held(int b) const {
+    const int n = kv_len[b], most = P.bt.max_pages * P.block;
+    if (n < 0 || n > most) {
+      record_status(P.status, FVATTN_ERR_INVALID_ARG);
+      return min(max(n, 0), most);
+    }
+    return n;
+  }
   // Steps of a unit of entry e and where it lies; 0 if the entry is not in use.
   __device__ int steps(long long e, int& b, int& m0, int& seen, Meta* m) const {
-    const Batch& bt = P.bt;
     if (P.kv_idx) {
-      const int r = static_cast<int>(e / P.c.H);
-      if (!sequence_of(bt, r, b)) return 0;
       int cnt = __ldg(P.kv_cnt + e);
-      if (cnt < 0 || cnt > bt.max_pages) {
-        record_status(P.status, FVATTN_ERR_INVALID_ARG);
-        cnt = min(max(cnt, 0), bt.max_pages);
+      const int r = static_cast<int>(e / P.c.H);
+      if (r >= cu[P.bt.B]) return 0;
+      int lo = 0, hi = P.bt.B;                  // cu[lo] <= r < cu[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cu[mid] <= r) lo = mid; else hi = mid;
       }
-      m0 = (r - __ldg(bt.cu + b)) * P.G;
+      b = lo;
+      if (cnt < 0 || cnt > P.bt.max_pages) {
+        record_status(P.status, FVATTN_ERR_INVALID_ARG);
+        cnt = min(max(cnt, 0), P.bt.max_pages);
+      }
+      m0 = (r - cu[b]) * P.G;
       if (m) {
-        m->cu = __ldg(bt.cu + b);
-        m->q = __ldg(bt.cu + b + 1) - m->cu;
-        m->n = held(bt, b, P.block, P.status);
+        m->cu = cu[b];
+        m->q = cu[b + 1] - m->cu;
+        m->n = held(b);
         const int pos = m->n - m->q + (r - m->cu);
         seen = P.causal ? min(max(pos + 1, 0), m->n) : m->n;
       }
       return max(1, (cnt * P.block + kStep - 1) / kStep);
     }
-    int lo = 0, hi = bt.B;
+    int lo = 0, hi = P.bt.B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (static_cast<long long>(__ldg(bt.cu + mid)) * P.G / RT + mid <= e) lo = mid; else hi = mid;
+      if (static_cast<long long>(cu[mid]) * P.G / RT + mid <= e) lo = mid; else hi = mid;
     }
     b = lo;
-    const int cu = __ldg(bt.cu + b);
-    const int q = min(__ldg(bt.cu + b + 1), bt.rows) - cu;
-    const long long first = (e - (static_cast<long long>(cu) * P.G / RT + b)) * RT;
+    const int r0 = cu[b], r1 = cu[b + 1];
+    const int q = min(r1, P.bt.rows) - r0;
+    const long long first = (e - (static_cast<long long>(r0) * P.G / RT + b)) * RT;
     if (q <= 0 || first >= static_cast<long long>(q) * P.G) return 0;
     m0 = static_cast<int>(first);
-    const int n = held(bt, b, P.block, P.status);
+    const int n = held(b);
     const int last = min((m0 + RT - 1) / P.G, q - 1);
-    seen = P.causal ? min(max(n - (__ldg(bt.cu + b + 1) - cu) + last + 1, 0), n) : n;
+    seen = P.causal ? min(max(n - (r1 - r0) + last + 1, 0), n) : n;
     if (m) {
-      m->cu = cu;
-      m->q = __ldg(bt.cu + b + 1) - cu;
+      m->cu = r0;
+      m->q = r1 - r0;
       m->n = n;
     }
     return max(1, (seen + kStep - 1) / kStep);
@@ -115,8 +146,10 @@ struct Piece {
 // Called by all threads of the block (has block barriers); at least `least` steps go to a
 // block that gets any.
 template <int RT, int kThreads>
-__device__ void find_piece(const AttnParams& P, Piece& sm, int least) {
-  const Entries<RT> en{P};
+__device__ void find_piece(const AttnParams& P, Seqs& seqs, Piece& sm, int least) {
+  seqs.load<kThreads>(P.bt);
+  __syncthreads();
+  const Entries<RT> en(P, seqs);
   const long long E = en.count();
   const int mult = en.times();
   const long long chunk = (E + kThreads - 1) / kThreads;
