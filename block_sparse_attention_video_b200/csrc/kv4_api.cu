@@ -186,8 +186,7 @@ fvattn_status fvattn_kv4_select(const fvattn_kv4_cache* cache, const fvattn_kv4_
   if (s != FVATTN_OK || batch->rows == 0) return s;
   auto hdr = static_cast<fvattn::WsHeader*>(workspace);
   return from_cuda(fvattn::kv4::launch_select(cache_of(cache), batch_of(batch), q, q_stride, Hq,
-                                              dtype == FVATTN_BF16, scale, p, k_min, cache->d, cache->block,
-                                              kv_idx, kv_cnt, &hdr->status, st));
+                                              dtype == FVATTN_BF16, scale, p, k_min, cache->d, cache->block, kv_idx, kv_cnt, &hdr->status, st));
 }
 
 fvattn_status fvattn_kv4_attn(const fvattn_kv4_cache* cache, const fvattn_kv4_batch* batch, const void* q,

@@ -2,166 +2,451 @@
 // pages before the row's own, averaged over the query heads of a KV head, then Top-p
 // with a Top-k floor.
 //
-// All arithmetic is fp64: the page sums are exact integers, so a score differs from
-// its definition by a few 2^-53 and only true ties are decided by rounding.
-#include "kv4.cuh"
+// All arithmetic is fp64: the page sums are exact integers and q is exact, so a score
+// differs from its definition by a few 2^-53 and only true ties are decided by rounding.
+//
+// One block per group of rows of a sequence and KV head. Up to eight (row, query head)
+// pairs share every page's sum, which is converted to fp64 once for all of them; what
+// bounds a call of many rows is the fp64 units (d multiply-adds a pair and page, 64 a
+// clock and SM), of single tokens HBM (4 d bytes a page).
+//   1. scores: fp64 tensor products of 8 pairs x 8 pages x 4 channels. q stays in registers;
+//      a page's sums are loaded straight into the operand's lanes (the order of channels in
+//      a dot product is free: lane t of a quad takes channels 16 i + 4 t .. + 3, 16 bytes).
+//   2. softmax of each pair over its pages and the mean over a row's pairs, in shared memory.
+//   3. per row one warp finds the smallest mass v* whose pages and those above reach p:
+//      a bracket of values is narrowed until at most 32 masses are left, which it sorts.
+//      Pages tied at v* are taken in index order. If the floor is larger, the k_min-th mass
+//      is found the same way on counts.
+#include "kv4_units.cuh"
 
 namespace fvattn {
 namespace kv4 {
 
 constexpr int kSelThreads = 256;
-
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_float(float x) { return x; }
 
-__device__ __forceinline__ double block_reduce(double v, bool max, double* red) {
+struct SelectParams {
+  Cache c;
+  Batch bt;
+  const void* q;
+  long long q_stride;
+  int G, RU, pairs;       // query heads per KV head; rows and (row, head) pairs per block
+  double w;               // scale / (1024 block)
+  float p;
+  int k_min, block, stride;   // stride: scores per row in shared memory (max_pages, whole tiles of 8)
+  int* kv_idx;
+  int* kv_cnt;
+  int* status;
+};
+
+__device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const double u = __shfl_xor_sync(0xffffffffu, v, o);
-    v = max ? fmax(v, u) : v + u;
-  }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = red[0];
-  for (int i = 1; i < kSelThreads / 32; ++i) v = max ? fmax(v, red[i]) : v + red[i];
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// One block per (row, KV head). Shared memory: scores and masses [n2] fp64, order [n2].
-template <typename T, int HD>
-__global__ void __launch_bounds__(kSelThreads)
-    select_kernel(const Cache c, const Batch bt, const T* __restrict__ q, long long q_stride, int G, double w,
-                  float p, int k_min, int block, int n2, int* __restrict__ kv_idx, int* __restrict__ kv_cnt,
-                  int* status) {
-  extern __shared__ double sh[];
-  double* x = sh;                 // scores of one query head
-  double* mass = sh + n2;
-  int* order = reinterpret_cast<int*>(sh + 2 * n2);
-  __shared__ double red[kSelThreads / 32];
-  __shared__ int s_cnt;
-  const int r = blockIdx.x / c.H, h = blockIdx.x % c.H;
-  if (blockIdx.x == 0 && threadIdx.x == 0 && __ldg(bt.cu + bt.B) > bt.rows)
-    record_status(status, FVATTN_ERR_INVALID_ARG);
-  int b;
-  if (!sequence_of(bt, r, b)) return;
-  const int n = held(bt, b, block, status);
-  const int pos = n - (__ldg(bt.cu + b + 1) - r);
-  const size_t unit = static_cast<size_t>(r) * c.H + h;
-  int* out = kv_idx + unit * bt.max_pages;
-  if (pos < 0 || pos >= n) {
-    if (threadIdx.x == 0) {
-      record_status(status, FVATTN_ERR_INVALID_ARG);
-      kv_cnt[unit] = 0;
-    }
-    return;
-  }
-  const int o = pos / block;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (c.k_scale) w *= static_cast<double>(__ldg(c.k_scale + h));
-  for (int j = threadIdx.x; j < n2; j += kSelThreads) mass[j] = j < o ? 0.0 : -1.0;
-  for (int g = 0; g < G; ++g) {
-    const T* qr = q + static_cast<long long>(r) * q_stride + (static_cast<long long>(h) * G + g) * HD;
-    double qv[HD / 32];
+// 32 values, one a lane, in descending order.
+__device__ __forceinline__ double sort32(double v) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < HD / 32; ++i) qv[i] = static_cast<double>(to_float(qr[i * 32 + lane]));
-    double mx = -INFINITY;
-    for (int j = warp; j < o; j += kSelThreads / 32) {
-      const int slot = pool_slot(bt, c.num_pages, b, j, status);
-      double s = 0.0;
-      if (slot >= 0) {
-        const int* ks = c.ksum + (static_cast<size_t>(slot) * c.H + h) * HD;
+  for (int size = 2; size <= 32; size <<= 1)
 #pragma unroll
-        for (int i = 0; i < HD / 32; ++i) s += qv[i] * static_cast<double>(__ldg(ks + i * 32 + lane));
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-      s *= w;
-      if (lane == 0) x[j] = s;
-      mx = fmax(mx, s);
-    }
-    mx = block_reduce(mx, true, red);
-    double z = 0.0;
-    for (int j = threadIdx.x; j < o; j += kSelThreads) {
-      x[j] = exp(x[j] - mx);
-      z += x[j];
-    }
-    z = block_reduce(z, false, red);
-    for (int j = threadIdx.x; j < o; j += kSelThreads) mass[j] += x[j] / z;
-    __syncthreads();
-  }
-  for (int j = threadIdx.x; j < n2; j += kSelThreads) {
-    if (j < o) mass[j] /= G;
-    order[j] = j;
-  }
-  // descending mass, ties by the lower page
-  for (int size = 2; size <= n2; size <<= 1)
     for (int stride = size >> 1; stride > 0; stride >>= 1) {
-      __syncthreads();
-      for (int t = threadIdx.x; t < n2 / 2; t += kSelThreads) {
-        const int lo = 2 * t - (t & (stride - 1)), hi = lo + stride;
-        const bool desc = (lo & size) == 0;
-        const double a = mass[lo], e = mass[hi];
-        const bool less = a < e || (a == e && order[lo] > order[hi]);
-        if (less == desc) {
-          mass[lo] = e; mass[hi] = a;
-          const int i = order[lo]; order[lo] = order[hi]; order[hi] = i;
-        }
-      }
+      const double u = __shfl_xor_sync(0xffffffffu, v, stride);
+      const bool first = (lane & stride) == 0, desc = (lane & size) == 0;
+      v = first == desc ? fmax(v, u) : fmin(v, u);
     }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    int np = o;
-    if (p < 1.f) {
-      double acc = 0.0;
-      for (int j = 0; j < o; ++j) {
-        acc += mass[j];
-        if (acc >= static_cast<double>(p)) { np = j + 1; break; }
-      }
-    }
-    s_cnt = min(o, max(np, k_min));
+  return v;
+}
+
+// What the search of a row's cut finds: the mass v* and the number of pages selected.
+struct Cut {
+  double star;
+  int cnt;
+};
+
+// The cut among at most 32 masses, one a lane, v descending: those above them number c_hi and
+// sum to f_hi. False if no prefix reaches p.
+__device__ __forceinline__ bool cut_sorted(double v, int in, int c_hi, double f_hi, double target, Cut& cut) {
+  const int lane = threadIdx.x & 31;
+  double sum = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double u = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += u;
   }
-  __syncthreads();
-  const int cnt = s_cnt;
-  for (int j = threadIdx.x; j < n2; j += kSelThreads) x[j] = 0.0;
-  __syncthreads();
-  for (int j = threadIdx.x; j < cnt; j += kSelThreads) x[order[j]] = 1.0;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    int m = 0;
-    for (int j = 0; j < o; ++j)
-      if (x[j] != 0.0) out[m++] = j;
-    out[m++] = o;
-    kv_cnt[unit] = m;
+  const unsigned reach = __ballot_sync(0xffffffffu, f_hi + sum >= target && lane < in);
+  if (reach == 0u) return false;
+  const int at = __ffs(reach) - 1;
+  cut.star = __shfl_sync(0xffffffffu, v, at);
+  cut.cnt = c_hi + at + 1;
+  return true;
+}
+
+// Puts the masses of a bracket one after the other: `m` is this lane's mass of 32, `in` whether it
+// belongs, `have` how many there are already; `box` holds 32.
+__device__ __forceinline__ void gather32(double m, bool in, double* box, int& have) {
+  const unsigned ins = __ballot_sync(0xffffffffu, in);
+  const int k = have + __popc(ins & ((1u << (threadIdx.x & 31)) - 1u));
+  if (in && k < 32) box[k] = m;
+  have += __popc(ins);
+}
+// This lane's one of the gathered masses, 0 behind the last.
+__device__ __forceinline__ double gathered(const double* box, int have) {
+  __syncwarp();
+  const int lane = threadIdx.x & 31;
+  const double v = lane < have ? box[lane] : 0.0;
+  __syncwarp();
+  return v;
+}
+
+// The cut, found in two stages. fp32 copies f of the masses narrow a bracket of values until at
+// most 32 masses are in it; a probe moves an end only where the fp32 sum is 2^-16 from p or
+// more (the sum of n <= 8192 rounded masses of total 1 is off by less than (n/32 + 7) 2^-24 <
+// 2^-15.9 at the worst and n / 2^29 as a rule; what it decides is checked in fp64). The masses
+// above the bracket are then added, and those inside sorted and added, in fp64. False if that
+// does not settle it.
+__device__ bool quick_cut(const double* x, const float* f, int n, float p, double* box, Cut& cut) {
+  const int lane = threadIdx.x & 31;
+  constexpr float kClear = 0x1p-16f;
+  float mx = 0.f;
+#pragma unroll 4
+  for (int j = lane; j < n; j += 32) mx = fmaxf(mx, f[j]);
+  // What lies below v* and v* itself sum to more than 1 - p: v* > (1 - p) / n.
+  unsigned lo = __float_as_uint((1.f - p) / n * 0.99f);
+  unsigned hi = __reduce_max_sync(0xffffffffu, __float_as_uint(mx)) + 1u;
+  int c_lo = n, c_hi = 0;                    // c_lo: an upper bound until a probe has moved lo
+  while (c_lo - c_hi > 32) {
+    if (hi <= lo + 1u) return false;
+    const unsigned mid = lo + ((hi - lo) >> 1);
+    const float v = __uint_as_float(mid);
+    float a = 0.f;
+    int c = 0;
+#pragma unroll 4
+    for (int j = lane; j < n; j += 32) {
+      const float m = f[j];
+      const bool ge = m >= v;
+      a += ge ? m : 0.f;
+      c += ge ? 1 : 0;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (a >= p + kClear) { lo = mid; c_lo = c; }
+    else if (a < p - kClear) { hi = mid; c_hi = c; }
+    else return false;
+  }
+  const float vlo = __uint_as_float(lo), vhi = __uint_as_float(hi);
+  double above = 0.0;
+  int have = 0;
+#pragma unroll 2
+  for (int j0 = 0; j0 < n; j0 += 32) {
+    const int j = j0 + lane;
+    const float m = j < n ? f[j] : -1.f;
+    const double d = j < n ? x[j] : 0.0;
+    if (m >= vhi) above += d;
+    gather32(d, m >= vlo && m < vhi, box, have);
+  }
+  above = warp_sum(above);
+  const double target = static_cast<double>(p);
+  if (have > 32 || above >= target) return false;
+  return cut_sorted(sort32(gathered(box, have)), have, c_hi, above, target, cut);
+}
+
+// The same for any n and any masses, in fp64 throughout: bisection of the bit patterns of
+// non-negative doubles. F(v) = the sum of the masses >= v, added up in a fixed order, falls
+// as v rises. by_count: the cut at `want` masses instead of at the sum p. False if no prefix
+// reaches p.
+__device__ bool full_cut(const double* x, int n, double target, bool by_count, int want, double* box, Cut& cut) {
+  using u64 = unsigned long long;
+  const int lane = threadIdx.x & 31;
+  auto bits_of = [](double v) { return static_cast<u64>(__double_as_longlong(v)); };
+  auto value_of = [](u64 b) { return __longlong_as_double(static_cast<long long>(b)); };
+  auto measure = [&](u64 bits, double& F, int& C) {
+    const double v = value_of(bits);
+    double a = 0.0;
+    int c = 0;
+    for (int j = lane; j < n; j += 32) {
+      const double m = x[j];
+      if (m >= v) {
+        a += m;
+        ++c;
+      }
+    }
+    F = warp_sum(a);
+    C = __reduce_add_sync(0xffffffffu, c);
+  };
+  double mx = 0.0;
+  for (int j = lane; j < n; j += 32) mx = fmax(mx, x[j]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmax(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  // bracket [lo, hi): c_lo masses at or above lo, c_hi (of sum f_hi) at or above hi
+  u64 lo = 0, hi = bits_of(mx) + 1;
+  int c_lo = n, c_hi = 0;
+  double F, f_hi = 0.0;
+  if (!by_count) {
+    measure(0, F, c_lo);
+    if (!(F >= target)) return false;
+  }
+  while (c_lo - c_hi > 32 && hi - lo > 1) {
+    const u64 mid = lo + ((hi - lo) >> 1);
+    int C;
+    measure(mid, F, C);
+    if (by_count ? C >= want : F >= target) { lo = mid; c_lo = C; } else { hi = mid; c_hi = C; f_hi = F; }
+  }
+  if (c_lo - c_hi > 32) {                    // equal masses, taken one by one
+    cut.star = value_of(lo);
+    int need = 1;
+    double acc = f_hi + cut.star;
+    while (acc < target && need < c_lo - c_hi) { acc += cut.star; ++need; }
+    cut.cnt = by_count ? want : c_hi + need;
+    return true;
+  }
+  int have = 0;
+  for (int j0 = 0; j0 < n; j0 += 32) {
+    const int j = j0 + lane;
+    const double m = j < n ? x[j] : 0.0;
+    gather32(m, j < n && bits_of(m) >= lo && bits_of(m) < hi, box, have);
+  }
+  const double v = sort32(gathered(box, have));
+  if (by_count) {
+    cut.star = __shfl_sync(0xffffffffu, v, want - c_hi - 1);
+    cut.cnt = want;
+    return true;
+  }
+  return cut_sorted(v, have, c_hi, f_hi, target, cut);
+}
+
+// Top-p with the floor on masses x[0..n), n >= 1: the selected pages ascending, then n itself.
+// Whole warp; every value that steers it is the same in all lanes.
+__device__ void pick_pages(const double* x, const float* f, int n, float p, int k_min, double* box, int* out,
+                           int* out_cnt) {
+  const int lane = threadIdx.x & 31;
+  const unsigned below = (1u << lane) - 1u;
+  Cut cut;
+  bool all = p >= 1.f || k_min >= n;
+  if (!all) {
+    bool found = quick_cut(x, f, n, p, box, cut);
+    if (!found) found = full_cut(x, n, static_cast<double>(p), false, 0, box, cut);
+    all = !found;
+    if (found && cut.cnt < k_min) full_cut(x, n, 2.0, true, k_min, box, cut);   // the floor
+  }
+  // all pages above v*, and at v* the first ones that fill the count
+  int above = 0;
+  if (!all) {
+    for (int j = lane; j < n; j += 32) above += x[j] > cut.star;
+    above = __reduce_add_sync(0xffffffffu, above);
+  }
+  const int take = all ? 0 : cut.cnt - above;
+  int written = 0, tied = 0;
+  for (int j0 = 0; j0 < n; j0 += 32) {
+    const int j = j0 + lane;
+    const double m = j < n ? x[j] : -1.0;
+    const bool eq = !all && m == cut.star;
+    const unsigned eqs = __ballot_sync(0xffffffffu, eq);
+    const bool sel = j < n && (all || m > cut.star || (eq && tied + __popc(eqs & below) < take));
+    const unsigned sels = __ballot_sync(0xffffffffu, sel);
+    if (sel) out[written + __popc(sels & below)] = j;
+    written += __popc(sels);
+    tied += __popc(eqs);
+  }
+  if (lane == 0) {
+    out[written] = n;
+    *out_cnt = written + 1;
   }
 }
 
+// C[8 x 8] += A[8 x 4] B[4 x 8] in fp64; a lane holds A[lane/4][lane%4], B[lane%4][lane/4] and
+// C[lane/4][2 (lane%4)], C[lane/4][2 (lane%4) + 1].
+__device__ __forceinline__ void mma_f64(double (&c)[2], double a, double b) {
+  asm("mma.sync.aligned.m8n8k4.row.col.f64.f64.f64.f64 {%0,%1}, {%2}, {%3}, {%0,%1};"
+      : "+d"(c[0]), "+d"(c[1])
+      : "d"(a), "d"(b));
+}
+
 template <typename T, int HD>
-static cudaError_t select_t(const Cache& c, const Batch& bt, const void* q, long long q_stride, int G, double w,
-                            float p, int k_min, int block, int* kv_idx, int* kv_cnt, int* status,
-                            cudaStream_t st) {
-  int n2 = 2;
-  while (n2 < bt.max_pages) n2 <<= 1;
-  const int smem = n2 * 20;
-  const long long grid = static_cast<long long>(bt.rows) * c.H;
+__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectParams P) {
+  constexpr int PAIRS = 8, kWarps = kSelThreads / 32;
+  extern __shared__ __align__(16) uint8_t raw[];
+  __shared__ __align__(16) double qs[PAIRS][HD + 2];   // two off: the quads' reads take all banks
+  __shared__ double scale[PAIRS];                      // 1 / (sum of a pair's exponentials * G)
+  __shared__ double box[kWarps][32];
+  __shared__ Seqs seqs;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = P.G, RU = P.RU, NP = P.pairs, LD = P.stride;
+  double* xs = reinterpret_cast<double*>(raw);                       // [NP][LD] scores
+  double* mass = G == 1 ? xs : xs + static_cast<size_t>(NP) * LD;    // [RU][LD]
+  float* fmass = reinterpret_cast<float*>(xs + static_cast<size_t>(NP + (G == 1 ? 0 : RU)) * LD);   // [RU][LD]
+  int* slots = reinterpret_cast<int*>(fmass + static_cast<size_t>(RU) * LD);                        // [LD]
+  seqs.load<kSelThreads>(P.bt);
+  __syncthreads();
+  const int* cu = P.bt.B <= Seqs::kMax ? seqs.cu : P.bt.cu;
+  if (blockIdx.x == 0 && tid == 0 && cu[P.bt.B] > P.bt.rows) record_status(P.status, FVATTN_ERR_INVALID_ARG);
+  // Groups are numbered without a prefix sum: sequence b owns those from cu[b]/RU + b on.
+  const int h = blockIdx.x % P.c.H, tile = blockIdx.x / P.c.H;
+  int lo = 0, hi = P.bt.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] / RU + mid <= tile) lo = mid; else hi = mid;
+  }
+  const int b = lo, r0 = cu[b], r1 = cu[b + 1];
+  const int first = r0 + (tile - (r0 / RU + b)) * RU;                // first row of the group
+  const int rows = min(RU, min(r1, P.bt.rows) - first);
+  if (first < r0 || rows <= 0) return;
+  const int n = held(P.bt, b, P.block, P.status);
+  const int pos0 = n - (r1 - first);                                 // position of the first row
+  const int most = pos0 + rows - 1 < 0 ? 0 : (pos0 + rows - 1) / P.block;   // pages to score
+  const double w = P.w * (P.c.k_scale ? static_cast<double>(__ldg(P.c.k_scale + h)) : 1.0);
+  const int chunks = (G + NP - 1) / NP;                              // of query heads; one if RU > 1
+  for (int j = tid; j < most; j += kSelThreads) slots[j] = pool_slot(P.bt, P.c.num_pages, b, j, P.status);
+  // Pages that row i of the group scores; 0 for a row before the sequence (recorded below).
+  auto own_of = [&](int i) { return i < rows && pos0 + i >= 0 ? (pos0 + i) / P.block : 0; };
+  for (int ch = 0; ch < chunks; ++ch) {
+    // pair k: row k / G, head k % G (RU rows), or head ch * NP + k of the one row
+    auto row_of = [&](int k) { return RU > 1 ? k / G : 0; };
+    auto head_of = [&](int k) { return RU > 1 ? k % G : ch * NP + k; };
+    auto live = [&](int k) { return k < NP && row_of(k) < rows && (RU > 1 ? k < RU * G : head_of(k) < G); };
+    for (int i = tid; i < PAIRS * HD; i += kSelThreads) {
+      const int k = i / HD, c = i % HD;
+      qs[k][c] = !live(k) ? 0.0
+                          : static_cast<double>(to_float(
+                                static_cast<const T*>(P.q)[static_cast<long long>(first + row_of(k)) * P.q_stride +
+                                                           (static_cast<long long>(h) * G + head_of(k)) * HD + c]));
+    }
+    __syncthreads();
+    // ---- scores: 8 pairs x 8 pages a warp and tile; a lane's channels are 16 i + 4 t .. + 3.
+    // The next tile's sums are on their way while this one's are multiplied.
+    {
+      const int g = lane >> 2, t = lane & 3;
+      const int* sums = P.c.ksum + static_cast<size_t>(h) * HD + 4 * t;
+      const size_t page = static_cast<size_t>(P.c.H) * HD;
+      int4 v[HD / 16];
+      auto fetch = [&](int j0) {
+        const int slot = j0 + g < most ? slots[j0 + g] : -1;
+        const int4* k4 = reinterpret_cast<const int4*>(sums + max(slot, 0) * page);
+#pragma unroll
+        for (int i = 0; i < HD / 16; ++i) v[i] = slot >= 0 ? __ldg(k4 + 4 * i) : make_int4(0, 0, 0, 0);
+      };
+      if (warp * 8 < most) fetch(warp * 8);
+#pragma unroll 1
+      for (int j0 = warp * 8; j0 < most; j0 += kWarps * 8) {
+        int4 u[HD / 16];
+#pragma unroll
+        for (int i = 0; i < HD / 16; ++i) u[i] = v[i];
+        if (j0 + kWarps * 8 < most) fetch(j0 + kWarps * 8);
+        double c[2][2] = {{0.0, 0.0}, {0.0, 0.0}};                   // two chains
+#pragma unroll
+        for (int i = 0; i < HD / 16; ++i) {
+          const double2 a0 = *reinterpret_cast<const double2*>(&qs[g][16 * i + 4 * t]);
+          const double2 a1 = *reinterpret_cast<const double2*>(&qs[g][16 * i + 4 * t + 2]);
+          mma_f64(c[0], a0.x, static_cast<double>(u[i].x));
+          mma_f64(c[1], a0.y, static_cast<double>(u[i].y));
+          mma_f64(c[0], a1.x, static_cast<double>(u[i].z));
+          mma_f64(c[1], a1.y, static_cast<double>(u[i].w));
+        }
+        // an invalid page (recorded) scores 0; the row of scores is padded to whole tiles
+        if (g < NP)
+          *reinterpret_cast<double2*>(&xs[static_cast<size_t>(g) * LD + j0 + 2 * t]) =
+              make_double2((c[0][0] + c[1][0]) * w, (c[0][1] + c[1][1]) * w);
+      }
+    }
+    __syncthreads();
+    // ---- softmax of each pair over the pages before its row's own: a warp per pair
+    if (warp < NP) {
+      const int own = live(warp) ? own_of(row_of(warp)) : 0;
+      double* x = xs + static_cast<size_t>(warp) * LD;
+      double mx = -INFINITY, z = 0.0;
+#pragma unroll 4
+      for (int j = lane; j < own; j += 32) mx = fmax(mx, x[j]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmax(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+#pragma unroll 2
+      for (int j = lane; j < own; j += 32) {
+        const double e = exp(x[j] - mx);
+        x[j] = e;
+        z += e;
+      }
+      z = warp_sum(z);
+      if (lane == 0) scale[warp] = z > 0.0 ? 1.0 / (z * G) : 0.0;
+    }
+    __syncthreads();
+    // ---- mean over the heads of each row
+    const int per = RU > 1 ? G : min(NP, G - ch * NP);               // pairs of a row in this chunk
+#pragma unroll 1
+    for (int i = 0; i < rows; ++i) {
+      const int own = own_of(i);
+      const double* x = xs + static_cast<size_t>(i) * per * LD;
+      for (int j = tid; j < own; j += kSelThreads) {
+        double m = ch > 0 ? mass[static_cast<size_t>(i) * LD + j] : 0.0;
+        for (int k = 0; k < per; ++k) m = fma(x[static_cast<size_t>(k) * LD + j], scale[i * per + k], m);
+        mass[static_cast<size_t>(i) * LD + j] = m;
+        fmass[static_cast<size_t>(i) * LD + j] = static_cast<float>(m);
+      }
+    }
+    __syncthreads();
+  }
+  // ---- one warp per row
+  for (int i = warp; i < rows; i += kWarps) {
+    const size_t unit = static_cast<size_t>(first + i) * P.c.H + h;
+    int* out = P.kv_idx + unit * P.bt.max_pages;
+    const int own = own_of(i);
+    if (own == 0) {
+      if (lane == 0) {
+        const bool before = pos0 + i < 0;
+        if (before) record_status(P.status, FVATTN_ERR_INVALID_ARG); else out[0] = 0;
+        P.kv_cnt[unit] = before ? 0 : 1;
+      }
+      continue;
+    }
+    pick_pages(mass + static_cast<size_t>(i) * LD, fmass + static_cast<size_t>(i) * LD, own, P.p, P.k_min, box[warp],
+               out, P.kv_cnt + unit);
+  }
+}
+
+// Shared memory of the scores, the masses (fp64 and fp32) and the pool slots.
+static size_t select_smem(int pairs, int ru, int G, int stride) {
+  return static_cast<size_t>(pairs + (G == 1 ? 0 : ru)) * stride * sizeof(double) +
+         static_cast<size_t>(ru + 1) * stride * sizeof(float);
+}
+
+template <typename T, int HD>
+static cudaError_t select_t(SelectParams& P, cudaStream_t st) {
+  // Up to eight (row, head) pairs a block, as shared memory holds them beside 13 KB of fixed
+  // size: eight up to 2,000 pages, down to one at 8,192.
+  P.pairs = 8;
+  while (P.pairs > 1 && select_smem(P.pairs, P.pairs > P.G ? P.pairs / P.G : 1, P.G, P.stride) > 208 * 1024) P.pairs /= 2;
+  P.RU = P.pairs > P.G ? P.pairs / P.G : 1;
+  if (P.RU == 1) P.pairs = min(P.pairs, P.G);
+  const long long grid = (static_cast<long long>(P.bt.rows) / P.RU + P.bt.B) * P.c.H;
   if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  const int smem = static_cast<int>(select_smem(P.pairs, P.RU, P.G, P.stride));
   cudaError_t e = cudaFuncSetAttribute(select_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  select_kernel<T, HD><<<static_cast<unsigned>(grid), kSelThreads, smem, st>>>(
-      c, bt, static_cast<const T*>(q), q_stride, G, w, p, k_min, block, n2, kv_idx, kv_cnt, status);
+  select_kernel<T, HD><<<static_cast<unsigned>(grid), kSelThreads, smem, st>>>(P);
   return cudaGetLastError();
 }
 
 cudaError_t launch_select(const Cache& c, const Batch& bt, const void* q, long long q_stride, int Hq, bool bf16,
                           float scale, float p, int k_min, int d, int block, int* kv_idx, int* kv_cnt,
                           int* status, cudaStream_t st) {
-  const int G = Hq / c.H;
-  const double w = static_cast<double>(scale) / (1024.0 * block);
-  if (d == 128)
-    return bf16 ? select_t<__nv_bfloat16, 128>(c, bt, q, q_stride, G, w, p, k_min, block, kv_idx, kv_cnt, status, st)
-                : select_t<float, 128>(c, bt, q, q_stride, G, w, p, k_min, block, kv_idx, kv_cnt, status, st);
-  return bf16 ? select_t<__nv_bfloat16, 64>(c, bt, q, q_stride, G, w, p, k_min, block, kv_idx, kv_cnt, status, st)
-              : select_t<float, 64>(c, bt, q, q_stride, G, w, p, k_min, block, kv_idx, kv_cnt, status, st);
+  SelectParams P;
+  P.c = c;
+  P.bt = bt;
+  P.q = q;
+  P.q_stride = q_stride;
+  P.G = Hq / c.H;
+  P.RU = P.pairs = 1;
+  P.w = static_cast<double>(scale) / (1024.0 * block);
+  P.p = p;
+  P.k_min = k_min;
+  P.block = block;
+  P.stride = (bt.max_pages + 7) & ~7;
+  P.kv_idx = kv_idx;
+  P.kv_cnt = kv_cnt;
+  P.status = status;
+  if (d == 128) return bf16 ? select_t<__nv_bfloat16, 128>(P, st) : select_t<float, 128>(P, st);
+  return bf16 ? select_t<__nv_bfloat16, 64>(P, st) : select_t<float, 64>(P, st);
 }
 
 }  // namespace kv4
