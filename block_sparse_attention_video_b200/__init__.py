@@ -214,6 +214,8 @@ def _expect_ws(ws, dev):
 def _call(dev, fn, *args):
     """Runs a library call with ``dev`` current, so that device-side lookups (SM count,
     static scratch) and launches happen on the tensors' device."""
+    if torch.cuda.current_device() == dev.index:      # the usual case; the switch costs microseconds
+        return fn(*args)
     with torch.cuda.device(dev):
         return fn(*args)
 

@@ -368,9 +368,20 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
         z += e;
       }
       z = warp_sum(z);
-      if (lane == 0) scale[warp] = z > 0.0 ? 1.0 / (z * G) : 0.0;
+      z = z > 0.0 ? 1.0 / (z * G) : 0.0;
+      if (G == 1) {                                                  // the pair's row: x is its masses' place
+#pragma unroll 4
+        for (int j = lane; j < own; j += 32) {
+          const double m = x[j] * z;
+          x[j] = m;
+          fmass[static_cast<size_t>(warp) * LD + j] = static_cast<float>(m);
+        }
+      } else if (lane == 0) {
+        scale[warp] = z;
+      }
     }
     __syncthreads();
+    if (G == 1) break;
     // ---- mean over the heads of each row
     const int per = RU > 1 ? G : min(NP, G - ch * NP);               // pairs of a row in this chunk
 #pragma unroll 1

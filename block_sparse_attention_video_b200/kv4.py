@@ -13,7 +13,7 @@ import math
 import torch
 
 from . import (FVATTN_OP_KV4_APPEND, FVATTN_OP_KV4_ATTN, FVATTN_OP_KV4_SELECT, _c_float, _c_int,
-               _c_size_t, _c_void_p, _call, _check, _dtype_code, _expect, _expect_ws, _lib, _ptr, _stream,
+               _c_size_t, _c_void_p, _call, _check, _dtype_code, _expect, _expect_ws, _lib, _stream,
                alloc_workspace)
 
 _c_int64 = ctypes.c_int64
@@ -50,7 +50,8 @@ _lib.fvattn_kv4_attn.restype = _c_int
 class KV4Cache:
     """A pool of ``num_pages`` pages of ``block`` tokens for ``H`` KV heads of ``d`` channels:
     ``pages`` [num_pages, H, block*(d+d/8)] uint8 and ``ksum`` [num_pages, H, d] int32 (allocated
-    here unless given), with optional fp32 head scales [H]."""
+    here unless given), with optional fp32 head scales [H]. The tensors stay the cache's for its
+    lifetime; their contents may change."""
 
     def __init__(self, num_pages, H, d, block, device="cuda", k_scale=None, v_scale=None, pages=None, ksum=None):
         dev = torch.device(device)
@@ -70,18 +71,22 @@ class KV4Cache:
         _expect(ksum, "ksum", dev, (num_pages, H, d), torch.int32)
         _expect(k_scale, "k_scale", dev, (H,), torch.float32, optional=True)
         _expect(v_scale, "v_scale", dev, (H,), torch.float32, optional=True)
-        self.pages, self.ksum, self.k_scale, self.v_scale = pages, ksum, k_scale, v_scale
+        self._tensors = (pages, ksum, k_scale, v_scale)
         self.device = dev
-
-    def _struct(self):
         p = lambda t: None if t is None else t.data_ptr()
-        return _CacheStruct(p(self.pages), p(self.ksum), p(self.k_scale), p(self.v_scale), self.num_pages, self.H,
-                            self.d, self.block)
+        self._struct = _CacheStruct(p(pages), p(ksum), p(k_scale), p(v_scale), self.num_pages, self.H, self.d, self.block)
+        self._ref = ctypes.byref(self._struct)
+
+    pages = property(lambda self: self._tensors[0])
+    ksum = property(lambda self: self._tensors[1])
+    k_scale = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
 
 
 class KV4Batch:
     """The sequences of a call: ``table`` [B, max_pages], ``kv_len`` [B] and ``cu`` [B+1], all int32
-    CUDA tensors, and ``max_q``, the most rows any of them has."""
+    CUDA tensors, and ``max_q``, the most rows any of them has. The tensors stay the batch's for its
+    lifetime; their contents may change."""
 
     def __init__(self, table, kv_len, cu, max_q):
         for t, name in ((table, "table"), (kv_len, "kv_len"), (cu, "cu")):
@@ -96,33 +101,42 @@ class KV4Batch:
         _expect(cu, "cu", dev, (B + 1,), torch.int32)
         if int(max_q) < 1:
             raise ValueError("max_q must be positive")
-        self.table, self.kv_len, self.cu, self.max_q = table, kv_len, cu, int(max_q)
-        self.B, self.max_pages, self.device = B, table.shape[1], dev
+        self._tensors = (table, kv_len, cu)
+        self.max_q, self.B, self.max_pages, self.device = int(max_q), B, table.shape[1], dev
+        self._args = (table.data_ptr(), kv_len.data_ptr(), cu.data_ptr(), self.B, self.max_pages)
 
-    def _struct(self, rows):
-        return _BatchStruct(self.table.data_ptr(), self.kv_len.data_ptr(), self.cu.data_ptr(), self.B, self.max_pages,
-                            int(rows), self.max_q)
+    table = property(lambda self: self._tensors[0])
+    kv_len = property(lambda self: self._tensors[1])
+    cu = property(lambda self: self._tensors[2])
+
+    def _ref(self, rows):
+        return ctypes.byref(_BatchStruct(*self._args, rows, self.max_q))
 
 
 def _rows(t, name, dev, heads, d, dtype=None):
     """A [rows, heads, d] input whose rows may lie apart (columns of a wider projection);
-    returns (rows, row stride in elements)."""
+    returns (rows, heads, row stride in elements, dtype code)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [rows, {heads or 'heads'}, {d}]")
-    _dtype_code(t)
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != d or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [rows, {heads or 'heads'}, {d}]")
+    code = _dtype_code(t)
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    rows, H = t.shape[0], t.shape[1]
-    if (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d):
+    rows, H = shape[0], shape[1]
+    if t.is_contiguous():
+        return rows, H, H * d, code
+    stride, head, one = t.stride()
+    if one != 1 or (H > 1 and head != d):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    stride = t.stride(0) if rows > 1 else H * d
+    if rows == 1:
+        stride = H * d
     if stride < H * d or (stride * t.element_size()) % 16:
         raise ValueError(f"{name}: row stride {stride} must be at least {H * d} and a multiple of 16 bytes")
-    return rows, stride
+    return rows, H, stride, code
 
 
 def _common(cache, batch, workspace):
@@ -138,37 +152,39 @@ def _lists(cache, batch, rows, kv_idx, kv_cnt):
 
 
 def _ws(workspace):
-    return _ptr(workspace), workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def fvattn_kv4_workspace_bytes(op: int, cache: KV4Cache, batch: KV4Batch, rows: int, H_q: int = 0) -> int:
-    """Workspace bytes of an FVATTN_OP_KV4_* call over ``rows`` rows with ``H_q`` query heads."""
-    c, b = cache._struct(), batch._struct(rows)   # the attention's grows with the batch's max_q
-    return int(_lib.fvattn_kv4_workspace_bytes(op, ctypes.byref(c), ctypes.byref(b), int(H_q)))
+    """Workspace bytes of an FVATTN_OP_KV4_* call over ``rows`` rows with ``H_q`` query heads (the
+    attention's grows with the batch's max_q)."""
+    return int(_lib.fvattn_kv4_workspace_bytes(op, cache._ref, batch._ref(int(rows)), int(H_q)))
 
 
 def fvattn_kv4_append(cache: KV4Cache, batch: KV4Batch, k, v, workspace, stream=None):
     """Quantizes k, v [rows, H, d] (bf16 or fp32) into the pages at the rows' positions."""
     dev = _common(cache, batch, workspace)
-    rows, ks = _rows(k, "k", dev, cache.H, cache.d)
-    vrows, vs = _rows(v, "v", dev, cache.H, cache.d, k.dtype)
+    rows, _, ks, code = _rows(k, "k", dev, cache.H, cache.d)
+    vrows, _, vs, _ = _rows(v, "v", dev, cache.H, cache.d, k.dtype)
     if vrows != rows:
         raise ValueError(f"v has {vrows} rows, k {rows}")
-    c, b = cache._struct(), batch._struct(rows)
-    _check(_call(dev, _lib.fvattn_kv4_append, ctypes.byref(c), ctypes.byref(b), _ptr(k), _ptr(v), ks, vs,
-                 _dtype_code(k), *_ws(workspace), _stream(stream, dev)), "fvattn_kv4_append")
+    _check(_call(dev, _lib.fvattn_kv4_append, cache._ref, batch._ref(rows), k.data_ptr(), v.data_ptr(), ks, vs,
+                 code, *_ws(workspace), _stream(stream, dev)), "fvattn_kv4_append")
     return cache
 
 
 def fvattn_kv4_read(cache: KV4Cache, batch: KV4Batch, k_out, v_out, workspace, stream=None):
     """Reads the rows back into k_out, v_out [rows, H, d] (bf16 or fp32, contiguous)."""
     dev = _common(cache, batch, workspace)
-    rows, _ = _rows(k_out, "k_out", dev, cache.H, cache.d)
-    _expect(k_out, "k_out", dev, (rows, cache.H, cache.d))
+    rows, _, _, code = _rows(k_out, "k_out", dev, cache.H, cache.d)
+    _expect(k_out, "k_out", dev)
     _expect(v_out, "v_out", dev, (rows, cache.H, cache.d), k_out.dtype)
-    c, b = cache._struct(), batch._struct(rows)
-    _check(_call(dev, _lib.fvattn_kv4_read, ctypes.byref(c), ctypes.byref(b), _ptr(k_out), _ptr(v_out),
-                 _dtype_code(k_out), *_ws(workspace), _stream(stream, dev)), "fvattn_kv4_read")
+    _check(_call(dev, _lib.fvattn_kv4_read, cache._ref, batch._ref(rows), k_out.data_ptr(), v_out.data_ptr(),
+                 code, *_ws(workspace), _stream(stream, dev)), "fvattn_kv4_read")
     return k_out, v_out
 
 
@@ -177,12 +193,11 @@ def fvattn_kv4_select(cache: KV4Cache, batch: KV4Batch, q, p: float, k_min: int,
     """The pages each row of q [rows, H_q, d] attends, per KV head: kv_idx [rows, H, max_pages] and
     kv_cnt [rows, H] (Top-p with a Top-k floor over the softmax on the pages' mean keys)."""
     dev = _common(cache, batch, workspace)
-    rows, qs = _rows(q, "q", dev, None, cache.d)
+    rows, H_q, qs, code = _rows(q, "q", dev, None, cache.d)
     _lists(cache, batch, rows, kv_idx, kv_cnt)
     sc = 1.0 / math.sqrt(cache.d) if scale is None else float(scale)
-    c, b = cache._struct(), batch._struct(rows)
-    _check(_call(dev, _lib.fvattn_kv4_select, ctypes.byref(c), ctypes.byref(b), _ptr(q), qs, q.shape[1],
-                 _dtype_code(q), sc, float(p), int(k_min), _ptr(kv_idx), _ptr(kv_cnt), *_ws(workspace),
+    _check(_call(dev, _lib.fvattn_kv4_select, cache._ref, batch._ref(rows), q.data_ptr(), qs, H_q, code, sc,
+                 float(p), int(k_min), kv_idx.data_ptr(), kv_cnt.data_ptr(), *_ws(workspace),
                  _stream(stream, dev)), "fvattn_kv4_select")
     return kv_idx, kv_cnt
 
@@ -192,17 +207,16 @@ def fvattn_kv4_attn(cache: KV4Cache, batch: KV4Batch, q, out, workspace, scale=N
     """Attention of q [rows, H_q, d] over the cache (or over the pages of the lists) into out, with
     an optional lse [rows, H_q] fp32."""
     dev = _common(cache, batch, workspace)
-    rows, qs = _rows(q, "q", dev, None, cache.d)
-    _expect(out, "out", dev, (rows, q.shape[1], cache.d), q.dtype)
-    _expect(lse, "lse", dev, (rows, q.shape[1]), torch.float32, optional=True)
+    rows, H_q, qs, code = _rows(q, "q", dev, None, cache.d)
+    _expect(out, "out", dev, (rows, H_q, cache.d), q.dtype)
+    _expect(lse, "lse", dev, (rows, H_q), torch.float32, optional=True)
     if (kv_idx is None) != (kv_cnt is None):
         raise ValueError("kv_idx and kv_cnt go together")
     if kv_idx is not None:
         _lists(cache, batch, rows, kv_idx, kv_cnt)
     sc = 1.0 / math.sqrt(cache.d) if scale is None else float(scale)
-    c, b = cache._struct(), batch._struct(rows)
-    _check(_call(dev, _lib.fvattn_kv4_attn, ctypes.byref(c), ctypes.byref(b), _ptr(q), qs, q.shape[1], _ptr(out),
-                 _ptr(lse), _dtype_code(q), sc, 1 if causal else 0, _ptr(kv_idx), _ptr(kv_cnt), *_ws(workspace),
+    _check(_call(dev, _lib.fvattn_kv4_attn, cache._ref, batch._ref(rows), q.data_ptr(), qs, H_q, out.data_ptr(),
+                 _at(lse), code, sc, 1 if causal else 0, _at(kv_idx), _at(kv_cnt), *_ws(workspace),
                  _stream(stream, dev)), "fvattn_kv4_attn")
     return out
 
@@ -226,10 +240,9 @@ class KV4Path:
             self.kv_idx = torch.empty((max_rows, cache.H, max_pages), dtype=torch.int32, device=dev)
             self.kv_cnt = torch.empty((max_rows, cache.H), dtype=torch.int32, device=dev)
         b = _BatchStruct(None, None, None, self.max_batch, self.max_pages, self.max_rows, self.max_rows)
-        c = cache._struct()
 
         def workspace(op):
-            n = int(_lib.fvattn_kv4_workspace_bytes(op, ctypes.byref(c), ctypes.byref(b), self.H_q))
+            n = int(_lib.fvattn_kv4_workspace_bytes(op, cache._ref, ctypes.byref(b), self.H_q))
             if n == 0:
                 raise ValueError("unsupported sizes")
             return alloc_workspace(n, dev)
