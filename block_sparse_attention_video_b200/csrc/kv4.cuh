@@ -36,9 +36,8 @@ struct Batch {
   int B, max_pages, rows;
 };
 
-// Tokens held by sequence b, clamped to what its table row can hold.
-__device__ __forceinline__ int held(const Batch& bt, int b, int block, int* status) {
-  const int n = __ldg(bt.kv_len + b);
+// A sequence's length n, clamped to what its table row can hold.
+__device__ __forceinline__ int held(int n, const Batch& bt, int block, int* status) {
   const int most = bt.max_pages * block;
   if (n < 0 || n > most) {
     record_status(status, FVATTN_ERR_INVALID_ARG);
@@ -55,18 +54,6 @@ __device__ __forceinline__ int pool_slot(const Batch& bt, int num_pages, int b, 
     return -1;
   }
   return s;
-}
-
-// Sequence of row r: the last b with cu[b] <= r. False for a row behind the last sequence.
-__device__ __forceinline__ bool sequence_of(const Batch& bt, int r, int& b) {
-  if (r >= __ldg(bt.cu + bt.B)) return false;
-  int lo = 0, hi = bt.B;                    // cu[lo] <= r < cu[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(bt.cu + mid) <= r) lo = mid; else hi = mid;
-  }
-  b = lo;
-  return true;
 }
 
 // Eight E2M1 codes (one 32-bit word, lowest channel in the low bits) to four f16 pairs.

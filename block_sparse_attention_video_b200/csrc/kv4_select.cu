@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
   int* slots = reinterpret_cast<int*>(fmass + static_cast<size_t>(RU) * LD);                        // [LD]
   seqs.load<kSelThreads>(P.bt);
   __syncthreads();
-  const int* cu = P.bt.B <= Seqs::kMax ? seqs.cu : P.bt.cu;
+  const int *cu = seqs.rows_of(P.bt), *kv_len = seqs.lengths_of(P.bt);
   if (blockIdx.x == 0 && tid == 0 && cu[P.bt.B] > P.bt.rows) record_status(P.status, FVATTN_ERR_INVALID_ARG);
   // Groups are numbered without a prefix sum: sequence b owns those from cu[b]/RU + b on.
   const int h = blockIdx.x % P.c.H, tile = blockIdx.x / P.c.H;
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
   const int first = r0 + (tile - (r0 / RU + b)) * RU;                // first row of the group
   const int rows = min(RU, min(r1, P.bt.rows) - first);
   if (first < r0 || rows <= 0) return;
-  const int n = held(P.bt, b, P.block, P.status);
+  const int n = held(kv_len[b], P.bt, P.block, P.status);
   const int pos0 = n - (r1 - first);                                 // position of the first row
   const int most = pos0 + rows - 1 < 0 ? 0 : (pos0 + rows - 1) / P.block;   // pages to score
   const double w = P.w * (P.c.k_scale ? static_cast<double>(__ldg(P.c.k_scale + h)) : 1.0);

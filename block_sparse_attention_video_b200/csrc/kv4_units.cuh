@@ -53,6 +53,8 @@ struct Seqs {
   static constexpr int kMax = 256;
   int cu[kMax + 1];
   int kv_len[kMax];
+  __device__ const int* rows_of(const Batch& bt) const { return bt.B <= kMax ? cu : bt.cu; }
+  __device__ const int* lengths_of(const Batch& bt) const { return bt.B <= kMax ? kv_len : bt.kv_len; }
   template <int kThreads>
   __device__ void load(const Batch& bt) {
     if (bt.B > kMax) return;
@@ -73,20 +75,12 @@ struct Entries {
   const int* cu;          // shared memory or global
   const int* kv_len;
   __device__ Entries(const AttnParams& p, const Seqs& s)
-      : P(p), cu(p.bt.B <= Seqs::kMax ? s.cu : p.bt.cu), kv_len(p.bt.B <= Seqs::kMax ? s.kv_len : p.bt.kv_len) {}
+      : P(p), cu(s.rows_of(p.bt)), kv_len(s.lengths_of(p.bt)) {}
   __device__ long long count() const {
     return P.kv_idx ? static_cast<long long>(P.bt.rows) * P.c.H
                     : static_cast<long long>(P.bt.rows) * P.G / RT + P.bt.B;
   }
   __device__ int times() const { return P.kv_idx ? (P.G + RT - 1) / RT : P.c.H; }
-  __device__ int held(int b) const {
-    const int n = kv_len[b], most = P.bt.max_pages * P.block;
-    if (n < 0 || n > most) {
-      record_status(P.status, FVATTN_ERR_INVALID_ARG);
-      return min(max(n, 0), most);
-    }
-    return n;
-  }
   // Steps of a unit of entry e and where it lies; 0 if the entry is not in use.
   __device__ int steps(long long e, int& b, int& m0, int& seen, Meta* m) const {
     if (P.kv_idx) {
@@ -107,7 +101,7 @@ struct Entries {
       if (m) {
         m->cu = cu[b];
         m->q = cu[b + 1] - m->cu;
-        m->n = held(b);
+        m->n = held(kv_len[b], P.bt, P.block, P.status);
         const int pos = m->n - m->q + (r - m->cu);
         seen = P.causal ? min(max(pos + 1, 0), m->n) : m->n;
       }
@@ -124,7 +118,7 @@ struct Entries {
     const long long first = (e - (static_cast<long long>(r0) * P.G / RT + b)) * RT;
     if (q <= 0 || first >= static_cast<long long>(q) * P.G) return 0;
     m0 = static_cast<int>(first);
-    const int n = held(b);
+    const int n = held(kv_len[b], P.bt, P.block, P.status);
     const int last = min((m0 + RT - 1) / P.G, q - 1);
     seen = P.causal ? min(max(n - (r1 - r0) + last + 1, 0), n) : n;
     if (m) {

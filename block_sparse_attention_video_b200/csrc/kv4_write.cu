@@ -3,16 +3,16 @@
 // of the cache to bf16 or fp32.
 //
 // Quantization of 16 channels x: s = E4M3 nearest to min(max|x| / 6, 448), code =
-// E2M1 nearest to x / s, ties to even. The codes are exact decisions: r = fl(1/s),
-// q0 = fl(x r), q = fl(q0 + r fl(x - q0 s)); the residual x - q0 s is exact (fma), so
-// q is x / s up to 2^-47 before its last rounding. Where x / s lies on a border t of
-// two codes (t s has at most 7 significant bits), q = t exactly. Where it does not, x
-// is at least one fp32 step away from t s, and because s < 2 (as a significand) that
-// is more than 1/1.875 = 0.53 steps of t, so q does not round onto t.
+// E2M1 nearest to x / s, ties to even. The codes are exact decisions: r = 1/s to 2^-22, q0 =
+// fl(x r), q = fl(q0 + r (x - q0 s)); the residual x - q0 s is exact (fma), so q is x / s up to
+// 2^-44 before its last rounding. Where x / s lies on a border t of two codes (t s has at most
+// 7 significant bits), q = t exactly. Where it does not, x is at least one fp32 step away from
+// t s, and because s < 2 (as a significand) that is more than 1/1.875 = 0.53 steps of t, so q
+// does not round onto t. The same holds for max|x| / 6 and the borders of E4M3.
 //
 // Both kernels move bytes: what bounds them is HBM (2 d es bytes of K and V a token
 // and head, d + d/8 bytes of codes and scales).
-#include "kv4.cuh"
+#include "kv4_units.cuh"
 #include "sm100.cuh"
 
 namespace fvattn {
@@ -20,21 +20,34 @@ namespace kv4 {
 
 constexpr int kWriteThreads = 256;
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// Eight elements as they lie in memory, and as fp32.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 w;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(u[i] << 16);
+      x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
   }
-}
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+};
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
                                             pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
@@ -44,26 +57,64 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
+// x / y for one y and many x: r = fl(1/y), q0 = fl(x r), then Markstein's correction
+// ("Computation of elementary functions on the IBM RISC System/6000", 1990) with the exact
+// residual of a fused multiply-add, twice: the first makes q faithful, the second correctly
+// rounded. For y in [2^-60, 2^60] and |x| <= most = 2^13 y, where larger ones saturate anyway.
+struct Divisor {
+  float y, r, most;
+  int kind;               // 0: y is 1 (no scale), 1: corrected product, 2: plain division
+  __device__ Divisor(const float* scales, int h) {
+    y = scales ? __ldg(scales + h) : 1.f;
+    r = 1.f / y;
+    kind = !scales ? 0 : y >= 0x1p-60f && y <= 0x1p60f ? 1 : 2;
+    most = 8192.f * y;    // infinite for huge y: then nothing is clamped
+  }
+  __device__ __forceinline__ float corrected(float x) const {
+    float q = x * r;
+    q = fmaf(fmaf(-q, y, x), r, q);
+    return fmaf(fmaf(-q, y, x), r, q);
+  }
+};
+
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // Eight channels of a row, the other half of the 16-channel group in the neighbouring
-// lane: codes (lowest channel in the low bits) and the group's scale code. `mask` names
-// the lanes that call this together.
-__device__ __forceinline__ uint32_t quantize8(float (&x)[8], float head_scale, unsigned mask, uint32_t& scale) {
-  if (head_scale != 1.f) {
+// lane: codes (lowest channel in the low bits) and the group's scale code. Whole warp.
+// The quotients m / 6 and x / s are corrected once: they are then x / s up to 2^-44 before
+// the last rounding, which is all that the borders need (above).
+template <typename T>
+__device__ __forceinline__ uint32_t quantize8(const Raw8<T>& raw, const Divisor& head, uint32_t& scale) {
+  float x[8];
+  raw.get(x);
+  float m = fabsf(x[0]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __fdiv_rn(x[i], head_scale);
+  for (int i = 1; i < 7; i += 2) m = fmax3(m, fabsf(x[i]), fabsf(x[i + 1]));
+  m = fmaxf(m, fabsf(x[7]));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  if (m > head.most) {    // infinities, and what saturates by far
+    m = head.most;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(x[i], -head.most), head.most);
   }
-  float m = 0.f;
+  if (head.kind == 1) {   // division is monotonic: the largest quotient is the largest's
+    m = head.corrected(m);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-  m = fmaxf(m, __shfl_xor_sync(mask, m, 1));
-  scale = float_to_e4m3(fminf(__fdiv_rn(m, 6.f), 448.f));
-  if (scale == 0u) return 0u;
+    for (int i = 0; i < 8; ++i) x[i] = head.corrected(x[i]);
+  } else if (head.kind == 2) {
+    m = m / head.y;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(x[i] / head.y, -8192.f), 8192.f);
+  }
+  float c = m * 0.166666672f;                 // fl(1/6)
+  c = fmaf(fmaf(-c, 6.f, m), 0.166666672f, c);
+  scale = float_to_e4m3(fminf(c, 448.f));     // 448 where an infinite m has made c a NaN
   const float s = e4m3_to_float(scale);
-  if (m > 4096.f) {   // keeps the residual finite; |x| >= 6 s is code 6 whatever it is
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(x[i], -4096.f), 4096.f);
-  }
-  const float r = __fdiv_rn(1.f, s);
+  const float r = scale == 0u ? 0.f : reciprocal(s);   // codes 0 where the scale is
   float q[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -73,97 +124,124 @@ __device__ __forceinline__ uint32_t quantize8(float (&x)[8], float head_scale, u
   return pack_e2m1x8(q);
 }
 
+// Adds eight stored values, in units of 2^-10, to integer sums. A value is a whole number
+// below 2^22 of them: added to 1.5 * 2^23 it stands in the low bits of the sum, whose own bits
+// (kMagic, once per call) are taken off at the end.
+constexpr uint32_t kMagic = 0x4B400000u;
+__device__ __forceinline__ void add8(uint32_t codes, uint32_t scale, uint32_t (&acc)[8]) {
+  uint32_t p[4];
+  e2m1x8_to_half2(codes, p);
+  const float s = e4m3_to_float(scale) * 1024.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
+    acc[2 * i] += __float_as_uint(fmaf(f.x, s, 12582912.f));
+    acc[2 * i + 1] += __float_as_uint(fmaf(f.y, s, 12582912.f));
+  }
+}
+
 // One block per (page of a sequence that the call's rows touch, KV head): quantizes the
 // rows that fall into the page, HD/8 lanes a row, and if the page is full then, adds up
-// its keys' codes (the older ones with them). Pages are enumerated without a prefix
-// sum: sequence b owns the tiles from cu[b]/block + 2b on, which leaves room for the
-// at most q/block + 2 pages that q rows touch. The sum is a sum of integers: exact and
+// its keys (the codes just made, and the older ones from the page). Pages are enumerated
+// without a prefix sum: sequence b owns the tiles from cu[b]/block + 2b on, which leaves room
+// for the at most q/block + 2 pages that q rows touch. The sum is one of integers: exact and
 // the same in any order.
 template <typename T, int HD>
-__global__ void __launch_bounds__(kWriteThreads)
+__global__ void __launch_bounds__(kWriteThreads, sizeof(T) == 2 ? 4 : 3)
     append_kernel(const Cache c, const Batch bt, const T* __restrict__ k, const T* __restrict__ v,
                   long long k_stride, long long v_stride, int block, int* status) {
   constexpr int LPR = HD / 8;                 // lanes per row
   constexpr int RPB = kWriteThreads / LPR;    // rows per pass of the block
+  __shared__ Seqs seqs;
+  seqs.load<kWriteThreads>(bt);
+  __syncthreads();
+  const int *cu = seqs.rows_of(bt), *kv_len = seqs.lengths_of(bt);
   const int h = blockIdx.x % c.H;
   const int tile = blockIdx.x / c.H;
-  if (blockIdx.x == 0 && threadIdx.x == 0 && __ldg(bt.cu + bt.B) > bt.rows)
-    record_status(status, FVATTN_ERR_INVALID_ARG);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && cu[bt.B] > bt.rows) record_status(status, FVATTN_ERR_INVALID_ARG);
   int lo = 0, hi = bt.B;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(bt.cu + mid) / block + 2 * mid <= tile) lo = mid; else hi = mid;
+    if (cu[mid] / block + 2 * mid <= tile) lo = mid; else hi = mid;
   }
   const int b = lo;
-  const int r0 = __ldg(bt.cu + b);
-  const int q = __ldg(bt.cu + b + 1) - r0;
+  const int r0 = cu[b];
+  const int q = cu[b + 1] - r0;
   if (q <= 0) return;
-  const int n = held(bt, b, block, status);
+  const int n = held(kv_len[b], bt, block, status);
   const int start = n - q;                    // position of row r0
   if (start < 0 && threadIdx.x == 0) record_status(status, FVATTN_ERR_INVALID_ARG);
   const int pg = max(start, 0) / block + tile - (r0 / block + 2 * b);
   const int first = max(start, pg * block);   // positions [first, last) of this block
-  const int last = min(n, (pg + 1) * block);
+  const int last = min(min(n, (pg + 1) * block), start + bt.rows - r0);   // rows of the tensors only
   if (first >= last) return;
   const int slot = pool_slot(bt, c.num_pages, b, pg, status);
   if (slot < 0) return;
   const Layout L(HD, block);
   uint8_t* rec = c.pages + (static_cast<size_t>(slot) * c.H + h) * L.rec;
-  const float ks = c.k_scale ? __ldg(c.k_scale + h) : 1.f;
-  const float vs = c.v_scale ? __ldg(c.v_scale + h) : 1.f;
+  const Divisor ks(c.k_scale, h), vs(c.v_scale, h);
   const int l = threadIdx.x % LPR, g = threadIdx.x / LPR;
-  const unsigned mask = 0x3u << ((threadIdx.x & 31) & ~1);   // the two lanes of a group
-  for (int pos = first + g; pos < last; pos += RPB) {
-    const int r = r0 + pos - start;
-    if (r >= bt.rows) break;
+  const bool full = c.ksum && last == (pg + 1) * block;      // block-uniform
+  uint32_t acc[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+  uint32_t added = 0u;
+  const T* kp = k + static_cast<long long>(r0 - start) * k_stride + h * HD + l * 8;   // of position 0
+  const T* vp = v + static_cast<long long>(r0 - start) * v_stride + h * HD + l * 8;
+  // 0, but not to the compiler: CUDA 12.9 passes a word of codes from the conversion that packs it
+  // on to the one that unpacks it without its upper half.
+  const uint32_t zero = static_cast<uint32_t>(block) >> 16;
+  Raw8<T> x, y, xn, yn;                       // a row's K and V, the next one's while it is quantized
+  int pos = first + g;
+  x.load(kp + static_cast<long long>(min(pos, last - 1)) * k_stride);
+  y.load(vp + static_cast<long long>(min(pos, last - 1)) * v_stride);
+  // a warp's rows go round together: lanes without one repeat the last row and store nothing
+  const int warp_first = first + (threadIdx.x & ~31) / LPR;
+  for (int base = warp_first; base < last; base += RPB, pos += RPB) {
     const int t = pos - pg * block;
-    float x[8];
-    uint32_t sc;
-    load8(k + static_cast<long long>(r) * k_stride + h * HD + l * 8, x);
-    uint32_t w = quantize8(x, ks, mask, sc);
-    *reinterpret_cast<uint32_t*>(rec + t * (HD / 2) + l * 4) = w;
-    if (!(l & 1)) rec[L.kscale() + t * (HD / kGroup) + (l >> 1)] = static_cast<uint8_t>(sc);
-    load8(v + static_cast<long long>(r) * v_stride + h * HD + l * 8, x);
-    w = quantize8(x, vs, mask, sc);
-    *reinterpret_cast<uint32_t*>(rec + L.vcodes() + t * (HD / 2) + l * 4) = w;
-    if (!(l & 1)) rec[L.vscale() + t * (HD / kGroup) + (l >> 1)] = static_cast<uint8_t>(sc);
-  }
-  if (!c.ksum || last != (pg + 1) * block) return;   // block-uniform
-  // The page is full. Its codes are read back: this block's own stores are visible to
-  // it after the barrier, the older ones came from earlier calls.
-  __shared__ int part[RPB][HD];
-  __syncthreads();
-  int acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int t = g; t < block; t += RPB) {
-    const uint32_t w = *reinterpret_cast<const volatile uint32_t*>(rec + t * (HD / 2) + l * 4);
-    const uint32_t sc = *reinterpret_cast<const volatile uint8_t*>(rec + L.kscale() + t * (HD / kGroup) + (l >> 1));
-    uint32_t p[4];
-    e2m1x8_to_half2(w, p);
-    const float s = e4m3_to_float(sc) * 1024.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
-      acc[2 * i] += __float2int_rn(f.x * s);          // a whole number below 2^22: exact
-      acc[2 * i + 1] += __float2int_rn(f.y * s);
+    const bool mine = pos < last;
+    if (base + RPB < last) {
+      const int next = min(pos + RPB, last - 1);
+      xn.load(kp + static_cast<long long>(next) * k_stride);
+      yn.load(vp + static_cast<long long>(next) * v_stride);
     }
+    uint32_t sc;
+    uint32_t w = quantize8(x, ks, sc);
+    if (mine) {
+      *reinterpret_cast<uint32_t*>(rec + t * (HD / 2) + l * 4) = w;
+      if (!(l & 1)) rec[L.kscale() + t * (HD / kGroup) + (l >> 1)] = static_cast<uint8_t>(sc);
+      if (full) {
+        add8(w | zero, sc, acc);
+        ++added;
+      }
+    }
+    w = quantize8(y, vs, sc);
+    if (mine) {
+      *reinterpret_cast<uint32_t*>(rec + L.vcodes() + t * (HD / 2) + l * 4) = w;
+      if (!(l & 1)) rec[L.vscale() + t * (HD / kGroup) + (l >> 1)] = static_cast<uint8_t>(sc);
+    }
+    x = xn;
+    y = yn;
   }
+  if (!full) return;
+  for (int t = g; t < first - pg * block; t += RPB, ++added)
+    add8(*reinterpret_cast<const uint32_t*>(rec + t * (HD / 2) + l * 4),
+         rec[L.kscale() + t * (HD / kGroup) + (l >> 1)], acc);
+  __shared__ uint32_t part[RPB][HD];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) part[g][l * 8 + i] = acc[i];
+  for (int i = 0; i < 8; ++i) part[g][l * 8 + i] = acc[i] - added * kMagic;
   __syncthreads();
   if (threadIdx.x < HD) {
-    int s = 0;
+    uint32_t s = 0u;
 #pragma unroll 8
     for (int i = 0; i < RPB; ++i) s += part[i][threadIdx.x];
-    c.ksum[(static_cast<size_t>(slot) * c.H + h) * HD + threadIdx.x] = s;
+    c.ksum[(static_cast<size_t>(slot) * c.H + h) * HD + threadIdx.x] = static_cast<int>(s);
   }
 }
 
 template <typename T>
-__device__ __forceinline__ void decode8(const uint8_t* codes, const uint8_t* scale, float head_scale, T* out) {
-  const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(codes));
-  const float s = e4m3_to_float(__ldg(scale));
+__device__ __forceinline__ void decode8(uint32_t codes, uint32_t scale, float head_scale, T* out) {
+  const float s = e4m3_to_float(scale);
   uint32_t p[4];
-  e2m1x8_to_half2(w, p);
+  e2m1x8_to_half2(codes, p);
   float x[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -174,41 +252,74 @@ __device__ __forceinline__ void decode8(const uint8_t* codes, const uint8_t* sca
   store8(out, x);
 }
 
-// HD/8 lanes per (row, KV head), neighbouring groups on neighbouring heads of a row so
-// that the outputs are written in one stream.
+// A block reads 8 (row, KV head) pairs for every group of HD/8 lanes, neighbouring groups on
+// neighbouring heads so that the outputs are written in one stream. Where the block's rows
+// lie is looked up once, a thread a row.
 template <typename T, int HD>
 __global__ void __launch_bounds__(kWriteThreads)
     read_kernel(const Cache c, const Batch bt, T* __restrict__ k_out, T* __restrict__ v_out, int block, int* status) {
-  constexpr int LPR = HD / 8;
-  const long long unit = static_cast<long long>(blockIdx.x) * (kWriteThreads / LPR) + threadIdx.x / LPR;
-  const int l = threadIdx.x % LPR;
-  if (blockIdx.x == 0 && threadIdx.x == 0 && __ldg(bt.cu + bt.B) > bt.rows)
-    record_status(status, FVATTN_ERR_INVALID_ARG);
-  const int r = static_cast<int>(unit / c.H);
-  const int h = static_cast<int>(unit - static_cast<long long>(r) * c.H);
-  if (r >= bt.rows) return;
-  int b;
-  if (!sequence_of(bt, r, b)) return;
-  const int n = held(bt, b, block, status);
-  const int pos = n - (__ldg(bt.cu + b + 1) - r);
-  int slot = -1;
-  if (pos >= 0 && pos < n) slot = pool_slot(bt, c.num_pages, b, pos / block, status);
-  else record_status(status, FVATTN_ERR_INVALID_ARG);
-  T* ko = k_out + static_cast<size_t>(unit) * HD + l * 8;
-  T* vo = v_out + static_cast<size_t>(unit) * HD + l * 8;
-  if (slot < 0) {
-    const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    store8(ko, z);
-    store8(vo, z);
-    return;
+  constexpr int LPR = HD / 8, GROUPS = kWriteThreads / LPR, EACH = 8, UNITS = GROUPS * EACH;
+  __shared__ int2 place[UNITS + 1];                   // pool slot (-1: invalid, -2: no row) and position in the page
+  __shared__ Seqs seqs;
+  seqs.load<kWriteThreads>(bt);
+  __syncthreads();
+  const int *cu = seqs.rows_of(bt), *kv_len = seqs.lengths_of(bt);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && cu[bt.B] > bt.rows) record_status(status, FVATTN_ERR_INVALID_ARG);
+  const unsigned H = static_cast<unsigned>(c.H), u0 = blockIdx.x * UNITS;
+  const unsigned row0 = u0 / H, rows = min(u0 + UNITS - 1, bt.rows * H - 1) / H - row0 + 1;
+  for (unsigned i = threadIdx.x; i < rows; i += kWriteThreads) {
+    const int r = static_cast<int>(row0 + i);
+    int slot = -2, t = 0;
+    if (r < cu[bt.B]) {
+      int lo = 0, hi = bt.B;                          // cu[lo] <= r < cu[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cu[mid] <= r) lo = mid; else hi = mid;
+      }
+      const int b = lo, n = held(kv_len[b], bt, block, status), pos = n - (cu[b + 1] - r);
+      slot = -1;
+      if (pos >= 0 && pos < n) slot = pool_slot(bt, c.num_pages, b, pos / block, status);
+      else record_status(status, FVATTN_ERR_INVALID_ARG);
+      t = pos >= 0 ? pos % block : 0;
+    }
+    place[i] = make_int2(slot, t);
   }
+  __syncthreads();
   const Layout L(HD, block);
-  const uint8_t* rec = c.pages + (static_cast<size_t>(slot) * c.H + h) * L.rec;
-  const int t = pos % block;
-  decode8(rec + t * (HD / 2) + l * 4, rec + L.kscale() + t * (HD / kGroup) + (l >> 1),
-          c.k_scale ? __ldg(c.k_scale + h) : 1.f, ko);
-  decode8(rec + L.vcodes() + t * (HD / 2) + l * 4, rec + L.vscale() + t * (HD / kGroup) + (l >> 1),
-          c.v_scale ? __ldg(c.v_scale + h) : 1.f, vo);
+  const int l = threadIdx.x % LPR, g = threadIdx.x / LPR;
+#pragma unroll
+  for (int part = 0; part < EACH; part += 4) {
+    uint32_t w[4][2], sc[4][2];
+    int slot[4];
+    unsigned head[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const unsigned u = u0 + (part + i) * GROUPS + g, r = u / H;
+      slot[i] = -2;
+      head[i] = u - r * H;
+      if (u < bt.rows * H) {
+        const int2 at = place[r - row0];
+        slot[i] = at.x;
+        if (at.x >= 0) {
+          const uint8_t* rec = c.pages + (static_cast<size_t>(at.x) * H + head[i]) * L.rec;
+          const int co = at.y * (HD / 2) + l * 4, so = at.y * (HD / kGroup) + (l >> 1);
+          w[i][0] = __ldg(reinterpret_cast<const uint32_t*>(rec + co));
+          sc[i][0] = __ldg(rec + L.kscale() + so);
+          w[i][1] = __ldg(reinterpret_cast<const uint32_t*>(rec + L.vcodes() + co));
+          sc[i][1] = __ldg(rec + L.vscale() + so);
+        } else {
+          w[i][0] = w[i][1] = sc[i][0] = sc[i][1] = 0u;   // zeros
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (slot[i] == -2) continue;
+      const size_t at = static_cast<size_t>(u0 + (part + i) * GROUPS + g) * HD + l * 8;
+      decode8(w[i][0], sc[i][0], c.k_scale ? __ldg(c.k_scale + head[i]) : 1.f, k_out + at);
+      decode8(w[i][1], sc[i][1], c.v_scale ? __ldg(c.v_scale + head[i]) : 1.f, v_out + at);
+    }
+  }
 }
 
 template <typename T>
@@ -228,7 +339,7 @@ static cudaError_t append_t(const Cache& c, const Batch& bt, const void* k, cons
 template <typename T>
 static cudaError_t read_t(const Cache& c, const Batch& bt, void* k, void* v, int d, int block, int* status,
                           cudaStream_t st) {
-  const long long per = kWriteThreads / (d / 8);
+  const long long per = kWriteThreads / (d / 8) * 8;
   const long long grid = (static_cast<long long>(bt.rows) * c.H + per - 1) / per;
   if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;
   T* kt = static_cast<T*>(k);

@@ -235,6 +235,27 @@ def test_extreme_inputs(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("scales", [[1e-25, 0.7], [3.3e20, 2.0 ** 60], [2.0 ** -60, 1.1e-3]])
+def test_head_scales_of_any_size(dtype, scales):
+    """The stored value is that of the correctly rounded quotient by the head's scale, saturated."""
+    c = Case([300], [300], 2, 64, 64, seed=30, dtype=dtype, scaled=True, fill=False)
+    c.ks.copy_(torch.tensor(scales))
+    c.cache.k_scale.copy_(c.ks)
+    k = c.k[0].float() * c.ks[:, None] * torch.logspace(-4, 4, 300)[:, None, None]
+    k[7, :, 0], k[8, :, 1] = math.inf, -math.inf
+    c.k = [k.to(dtype)]
+    c.append(c.kv)
+    kc, ks, _, _ = c.records()
+    x = c.k[0].float().numpy()
+    want, sc = O.quantize(np.clip(x, -3e38, 3e38), c.ks.numpy())
+    for t in range(300):
+        slot, at = c.table_np[0, t // 64], t % 64
+        g, w = kc[slot, :, at], want[t]
+        assert np.array_equal(ks[slot, :, at], sc[t]), t
+        assert np.all((g == w) | (((g & 7) == 0) & ((w & 7) == 0))), t
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("d,block", [(64, 64), (128, 128), (128, 64)])
 def test_every_code_border(dtype, d, block):
     """x on and one step beside every border t * s of two codes, for every scale significand."""
