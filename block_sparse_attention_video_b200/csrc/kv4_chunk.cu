@@ -13,11 +13,10 @@
 //   warp  8          TMEM allocator and MMA issuer (whole warp, one elected lane issues)
 //   warp  9          producer: walks the units, copies each page's K and V halves (codes and
 //                    scales, 9 KB at d 128) into a ring of three
-//   warps 10-11      idle
-//   warps 12-15      expand the codes to f16 tiles in the 128-byte-swizzled layout of the
+//   warps 10-15      expand the codes to f16 tiles in the 128-byte-swizzled layout of the
 //                    MMA descriptors, 64 columns a half; E2M1 times E4M3 is exact in f16
 // The block launches with 128 registers a thread (512 x 128 = 65,536); the softmax
-// warpgroups rise to 184 and the others drop to 72 (2 x 128 x (184 + 72) = 65,536).
+// warpgroups rise to 184, the others drop to 72 (128 x 2 x (184 + 72) = 65,536).
 //
 // MMA order: S0(0) S1(0), then for k >= 1: PV0(k-1) S0(k) PV1(k-1) S1(k), at last PV0 PV1:
 // the exponentials of one slot overlap the other slot's products. TMEM (512 columns): S0
@@ -41,6 +40,7 @@ constexpr int kThreads = 512;
 constexpr int kRows = 256;
 constexpr int kRegsSoftmax = 184;
 constexpr int kRegsOther = 72;
+constexpr int kExpand = 6;      // warps that expand codes
 constexpr int kTiles = 4;       // expanded K and V tiles
 constexpr int kRaw = 3;         // raw K and V halves
 constexpr int kFlags = 8;       // steps whose page validity is kept: more than are in flight
@@ -85,6 +85,24 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&w)[4]) {
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+  uint16_t h;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(addr));
+  return h;
+}
+__device__ __forceinline__ int lds_s32(const int* p) {
+  int v;
+  asm volatile("ld.shared.s32 %0, [%1];" : "=r"(v) : "r"(smem_u32(p)));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, const uint32_t (&w)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+               : "memory");
 }
 
 // ------------------------------------------------------------------ producer
@@ -190,12 +208,13 @@ template <int HD>
 __device__ void expand(const AttnParams& P, Smem<HD>& sm) {
   constexpr int LPR = HD / 32;                     // lanes per row
   constexpr int RPW = 32 / LPR;                    // rows per warp and pass
-  const int warp = (threadIdx.x >> 5) - 12, lane = threadIdx.x & 31;
+  const int warp = (threadIdx.x >> 5) - (16 - kExpand), lane = threadIdx.x & 31;
   volatile int* abort_flag = &sm.abort_flag;
   const Layout L(HD, P.block);
   const int half = L.codes + L.scales;
   const int part = lane % LPR;
   const bool swap = part >= 2;
+  const int shift = P.block == 128 ? 7 : 6;
   int op = 0, un = 0, step = 0;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, P.status));
@@ -213,39 +232,42 @@ __device__ void expand(const AttnParams& P, Smem<HD>& sm) {
       for (int t = 0; t < 2; ++t, ++op) {
         const int rs = op % kRaw, ts = op % kTiles;
         if (!wait(&sm.raw_full[rs], (op / kRaw) & 1)) return;
-        const int absent = *reinterpret_cast<volatile int*>(&sm.flags[step % kFlags]);
+        const int absent = lds_s32(&sm.flags[step % kFlags]);
         if (!wait(&sm.kv_empty[ts], ((op / kTiles) & 1) ^ 1)) return;
-        const uint8_t* raw = sm.raw[rs];
-        const uint32_t dst = smem_u32(sm.kv[ts]);
-#pragma unroll 2
-        for (int r0 = warp * RPW; r0 < kStep; r0 += 4 * RPW) {
-          const int row = r0 + lane / LPR;
-          const int pg = row / P.block, key = row - pg * P.block;
-          const uint8_t* src = raw + pg * half;
-          uint4 w = *reinterpret_cast<const uint4*>(src + key * (HD / 2) + part * 16);
-          uint32_t sc = *reinterpret_cast<const uint16_t*>(src + L.codes + key * (HD / kGroup) + part * 2);
+        const uint32_t raw = smem_u32(sm.raw[rs]), dst = smem_u32(sm.kv[ts]) + (part >> 1) * Tile<HD>::kHalfBytes;
+        // all of the warp's rows are loaded first: the chains of conversions then overlap
+        constexpr int kGroups = kStep / RPW, kRounds = (kGroups + kExpand - 1) / kExpand;
+        uint32_t w[kRounds][4], sc[kRounds];
+#pragma unroll
+        for (int i = 0; i < kRounds; ++i) {
+          if (warp + kExpand * i >= kGroups) break;
+          const int row = (warp + kExpand * i) * RPW + lane / LPR;
+          const int pg = row >> shift, key = row & (P.block - 1);
+          const uint32_t src = raw + pg * half;
+          lds128(src + key * (HD / 2) + part * 16, w[i]);
+          sc[i] = lds_u16(src + L.codes + key * (HD / kGroup) + part * 2);
           // V behind the last key that a row sees, or of an absent page, is 0: memory there holds
           // anything, and P = 0 times NaN would not be 0
-          if (t == 1 && (s * kStep + row >= seen || ((absent >> pg) & 1))) sc = 0;
-          if (swap) {
-            w = make_uint4(w.z, w.w, w.x, w.y);
-            sc = (sc >> 8) | (sc << 8);
-          }
-          const __half2 hs = e4m3x2_to_half2(sc);
+          if (t == 1 && (s * kStep + row >= seen || ((absent >> pg) & 1))) sc[i] = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < kRounds; ++i) {
+          if (warp + kExpand * i >= kGroups) break;
+          const int row = (warp + kExpand * i) * RPW + lane / LPR;
+          const __half2 hs = e4m3x2_to_half2(sc[i]);
           const uint32_t h = *reinterpret_cast<const uint32_t*>(&hs);
-          const uint32_t f[2] = {__byte_perm(h, 0, 0x1010), __byte_perm(h, 0, 0x3232)};
-          const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-          const uint32_t base = dst + (part >> 1) * Tile<HD>::kHalfBytes + row * 128;
+          const uint32_t f[2] = {__byte_perm(h, 0, swap ? 0x3232 : 0x1010), __byte_perm(h, 0, swap ? 0x1010 : 0x3232)};
+          const uint32_t words[4] = {swap ? w[i][2] : w[i][0], swap ? w[i][3] : w[i][1], swap ? w[i][0] : w[i][2],
+                                     swap ? w[i][1] : w[i][3]};
+          const uint32_t base = dst + row * 128;
+          const int c0 = (part & 1) * 4, r7 = row & 7;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int y = 0; y < 4; ++y) {
             uint32_t v[4];
-            e2m1x8_to_half2(words[i], v);
+            e2m1x8_to_half2(words[y], v);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) v[y] = mul2(v[y], f[i >> 1]);
-            const int chunk = ((part & 1) * 4 + (swap ? (i ^ 2) : i)) ^ (row & 7);
-            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(base + chunk * 16), "r"(v[0]), "r"(v[1]),
-                         "r"(v[2]), "r"(v[3])
-                         : "memory");
+            for (int z = 0; z < 4; ++z) v[z] = mul2(v[z], f[y >> 1]);
+            sts128(base + (((c0 + (swap ? (y ^ 2) : y)) ^ r7) * 16), v);
           }
         }
         fence_async_shared();
@@ -353,24 +375,34 @@ __device__ void softmax(const AttnParams& P, Smem<HD>& sm, uint32_t tmem) {
   while (true) {
     const int u = un & 1;
     if (!wait(&sm.unit_full[u], (un >> 1) & 1)) return;
-    const Meta& m = sm.unit[u];
-    const int ns = m.ns, s0 = m.s0, mc = m.mc, m0 = m.m0, h = m.h, cu = m.cu, nq = m.q, n = m.n;
-    const int begin = m.begin, end = m.end;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.unit_empty[u]);
+    const Meta& m = sm.unit[u];                      // kept until the unit's end, read again there
+    const int ns = m.ns;
+    if (ns == 0 || X * 128 >= m.mc) {                // no unit, or no rows in this slot: warp-uniform
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.unit_empty[u]);
+      ++un;
+      if (ns == 0) return;
+      step += ns;
+      continue;
+    }
     ++un;
-    if (ns == 0) return;
-    if (X * 128 >= mc) { step += ns; continue; }     // this slot has no rows: warp-uniform
-    const int rr = X * 128 + row;
-    const bool live = rr < mc;
-    const int i_row = live ? (m0 + rr) / P.G : 0;
-    const size_t head = static_cast<size_t>(h) * P.G + (live ? (m0 + rr) - i_row * P.G : 0);
+    // this thread's row of the call's tensors and query head
+    auto place = [&](int& i_row, int& head) -> bool {
+      const int rr = X * 128 + row;
+      const bool live = rr < m.mc;
+      i_row = live ? (m.m0 + rr) / P.G : 0;
+      head = m.h * P.G + (live ? (m.m0 + rr) - i_row * P.G : 0);
+      return live;
+    };
+    float cs;                                        // logits per unit of S
+    int left;                                        // keys that the row sees from this step on
     // ---- Q: this thread's row, scaled so that its largest element lies in [2^13, 2^14)
-    int ex = 0;
     {
+      int i_row, head, ex = 0;
+      const bool live = place(i_row, head);
       uint4 w[HD / 8];
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(P.q) +
-                                                        static_cast<long long>(cu + i_row) * P.q_stride + head * HD);
+                                                        static_cast<long long>(m.cu + i_row) * P.q_stride + head * HD);
       float mx = 0.f;
 #pragma unroll
       for (int i = 0; i < HD / 8; ++i) {
@@ -398,24 +430,23 @@ __device__ void softmax(const AttnParams& P, Smem<HD>& sm, uint32_t tmem) {
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.q_full[X]);
+      const float base = P.scale_log2 * (P.c.k_scale ? __ldg(P.c.k_scale + m.h) : 1.f);
+      // never 0, so that a masked key's -inf stays -inf
+      cs = fmaxf(base * exp2f(static_cast<float>(-(ex / 2))) * exp2f(static_cast<float>(-(ex - ex / 2))), FLT_MIN);
+      const int n = m.n;
+      left = (live ? (P.causal ? min(max(n - m.q + i_row + 1, 0), n) : n) : 0) - m.s0 * kStep;
     }
-    const float base = P.scale_log2 * (P.c.k_scale ? __ldg(P.c.k_scale + h) : 1.f);
-    // logits per unit of S; never 0, so that a masked key's -inf stays -inf
-    const float cs = fmaxf(base * exp2f(static_cast<float>(-(ex / 2))) * exp2f(static_cast<float>(-(ex - ex / 2))), FLT_MIN);
-    const int pos = n - nq + i_row;
-    const int see = live ? (P.causal ? min(max(pos + 1, 0), n) : n) : 0;
     float mref = kFloor, l_run = 0.f;
 #pragma unroll 1
-    for (int k = 0; k < ns; ++k, ++step) {
+    for (int k = 0; k < ns; ++k, ++step, left -= kStep) {
       if (!wait(&sm.s_full[X], sn & 1)) return;
       ++sn;
       tc_fence_after();
-      const int absent = *reinterpret_cast<volatile int*>(&sm.flags[step % kFlags]) & (kStep / P.block == 2 ? 3 : 1);
+      const int absent = lds_s32(&sm.flags[step % kFlags]) & (kStep / P.block == 2 ? 3 : 1);
       uint32_t s[4][32];
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
       tmem_wait_ld();
-      const int left = see - (s0 + k) * kStep;       // keys of this step that the row sees
       if (__any_sync(0xffffffffu, left < kStep || absent != 0)) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -482,8 +513,13 @@ __device__ void softmax(const AttnParams& P, Smem<HD>& sm, uint32_t tmem) {
     if (!wait(&sm.o_full[X], on & 1)) return;
     ++on;
     tc_fence_after();
-    const float vs = P.c.v_scale ? __ldg(P.c.v_scale + h) : 1.f;
-    const size_t at = static_cast<size_t>(cu + i_row) * P.c.H * P.G + head;
+    int i_row, head;
+    const bool live = place(i_row, head);
+    const int begin = m.begin, end = m.end;
+    const float vs = P.c.v_scale ? __ldg(P.c.v_scale + m.h) : 1.f;
+    const size_t at = static_cast<size_t>(m.cu + i_row) * P.c.H * P.G + head;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.unit_empty[u]);
     __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(P.out) + at * HD;
     if (begin == end) {
       const float inv = l_run > 0.f || l_run != l_run ? vs / l_run : 0.f;
@@ -584,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const AttnParam
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.unit_full[i], 1);
-      mbar_init(&sm.unit_empty[i], 13);      // 8 softmax warps, 4 expanding, the issuer
+      mbar_init(&sm.unit_empty[i], 9 + kExpand);   // 8 softmax warps, the issuer, those that expand
       mbar_init(&sm.q_full[i], 4);
       mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.p_full[i][0], 4);
@@ -594,10 +630,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const AttnParam
     }
     for (int i = 0; i < kRaw; ++i) {
       mbar_init(&sm.raw_full[i], 1);
-      mbar_init(&sm.raw_empty[i], 4);
+      mbar_init(&sm.raw_empty[i], kExpand);
     }
     for (int i = 0; i < kTiles; ++i) {
-      mbar_init(&sm.kv_full[i], 4);
+      mbar_init(&sm.kv_full[i], kExpand);
       mbar_init(&sm.kv_empty[i], 1);
     }
     mbar_init(&sm.mma_done, 1);
@@ -632,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const AttnParam
     regs_dec<kRegsOther>();
     if (warp == 8) issue<HD>(P, sm, tmem);
     else if (warp == 9) produce<HD>(P, sm);
-    else if (warp >= 12) expand<HD>(P, sm);
+    else expand<HD>(P, sm);
     teardown();
     return;
   }
