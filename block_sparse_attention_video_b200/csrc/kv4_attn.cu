@@ -35,7 +35,9 @@ namespace kv4 {
 constexpr int kConsumers = 4;                       // consumer warps
 constexpr int kTiles = 2;                           // tiles of 16 keys a warp and step
 constexpr int kThreads = (kConsumers + 1) * 32;
-constexpr int kLeast = 4;                           // steps a block takes at least: joining costs about as much
+// Steps a block takes at least: joining costs about as much. (One of the fp32 path's, which
+// take three times as long.)
+constexpr int kLeast = 4;
 static_assert(kStep == kConsumers * kTiles * 16, "");
 
 template <int HD, int NT>
@@ -51,7 +53,7 @@ template <int HD, int NT>
 struct __align__(128) AttnSmem {
   using S = Shape<HD, NT>;
   uint8_t ring[S::kStages][S::kStageBytes];
-  float slab[kConsumers][S::RT][HD];
+  float slab[kConsumers][S::RT][HD + 2];
   float mx[2][kConsumers][S::RT];
   float sum[2][kConsumers][S::RT];
   int4 step[S::kStages];  // first keys of the stage's two pages (-1: no such page), -, unit ends here
@@ -123,8 +125,7 @@ __device__ void produce(const AttnParams& P, AttnSmem<HD, NT>& sm) {
     m.s0 = 0;
     if (x == lo) {
       steps = max(1, en.steps(entry, b, m0, seen, &m));
-      which = static_cast<int>(sm.piece.rem / steps);
-      m.s0 = static_cast<int>(sm.piece.rem - static_cast<long long>(which) * steps);
+      which = static_cast<int>(divide(sm.piece.rem, steps, m.s0));
     } else if (++which == mult) {
       which = 0;
       do ++entry; while (entry < E && (steps = en.steps(entry, b, m0, seen, &m)) == 0);
@@ -135,7 +136,7 @@ __device__ void produce(const AttnParams& P, AttnSmem<HD, NT>& sm) {
     }
     int cnt;                                       // pages of the unit
     if (P.kv_idx) {
-      m.h = static_cast<int>(entry % P.c.H);
+      divide(entry, P.c.H, m.h);
       m.m0 = m0 + which * RT;
       m.mc = min(RT, P.G - which * RT);
       cnt = min(max(__ldg(P.kv_cnt + entry), 0), P.bt.max_pages);
@@ -148,8 +149,8 @@ __device__ void produce(const AttnParams& P, AttnSmem<HD, NT>& sm) {
     }
     m.seen = seen;
     m.ns = static_cast<int>(min(static_cast<long long>(steps - m.s0), hi - x));
-    m.begin = piece_of(x - m.s0, total, sm.piece.blocks);
-    m.end = piece_of(x - m.s0 + steps - 1, total, sm.piece.blocks);
+    m.begin = x - m.s0 >= lo ? static_cast<int>(blockIdx.x) : piece_of(x - m.s0, total, sm.piece.blocks);
+    m.end = x - m.s0 + steps <= hi ? static_cast<int>(blockIdx.x) : piece_of(x - m.s0 + steps - 1, total, sm.piece.blocks);
     // Pool slots of 32 pages of the unit at a time, one a lane, and the first key of each.
     int window = (m.s0 * per) >> 5, w_slot = -1, w_key = -1;
     auto look_up = [&]() {
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : sizeof(T) == 4 ? 1 : 2
     sm.abort_flag = 0;
     fence_mbarrier_init();
   }
-  find_piece<RT, kThreads>(P, sm.seqs, sm.piece, kLeast);
+  find_piece<RT, kThreads>(P, sm.seqs, sm.piece, kExact ? 1 : kLeast);
   const int len = static_cast<int>(sm.piece.hi - sm.piece.lo);
   if (len <= 0) return;
   if (warp == kConsumers) {
@@ -545,8 +546,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : sizeof(T) == 4 ? 1 : 2
           for (int y = 0; y < 2; ++y)
             fn(j * 8 + 2 * t + y, g * (HD / 8) + 2 * i, o[j][i][y], o[j][i][2 + y], f[j][y]);
     };
+    // Shared memory holds row 2t + y as row 4y + t and turns a lane group's HD/8 channels by
+    // 2g: the stores of a warp then go to different banks.
+    auto row_at = [](int row) { return (row & ~7) | ((row & 1) << 2) | ((row >> 1) & 3); };
+    auto ch_at = [](int ch) {
+      constexpr int W = HD / 8;
+      return (ch & ~(W - 1)) | ((ch + 2 * (ch / W)) & (W - 1));
+    };
     each([&](int row, int ch, float a, float b, float fac) {
-      *reinterpret_cast<float2*>(&sm.slab[warp][row][ch]) = make_float2(a * fac, b * fac);
+      *reinterpret_cast<float2*>(&sm.slab[warp][row_at(row)][ch_at(ch)]) = make_float2(a * fac, b * fac);
     });
     if (!meet()) return;
     const bool whole = begin == end;
@@ -578,8 +586,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : sizeof(T) == 4 ? 1 : 2
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kConsumers; ++w) {
-        const float4 a = *reinterpret_cast<const float4*>(&sm.slab[w][row][ch]);
-        v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
+        const float2 a = *reinterpret_cast<const float2*>(&sm.slab[w][row_at(row)][ch_at(ch)]);
+        const float2 c = *reinterpret_cast<const float2*>(&sm.slab[w][row_at(row)][ch_at(ch + 2)]);
+        v.x += a.x; v.y += a.y; v.z += c.x; v.w += c.y;
       }
       if (whole) {
         finish(row, ch, v, mx, sum);
@@ -593,15 +602,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : sizeof(T) == 4 ? 1 : 2
     }
     if (whole) continue;
     // ---- the unit lies in blocks begin .. end: the last to arrive joins them in order
-    __threadfence();
+    // (one thread's fences, between the barriers, cover the whole block's stores and loads)
     if (!meet()) return;
     if (threadIdx.x == 0) {
+      __threadfence();
       sm.joiner = atomicAdd(P.arrived + begin, 1) == end - begin;
       __threadfence();
     }
     if (!meet()) return;
     if (!sm.joiner) continue;
-    __threadfence();
     auto part_of = [&](int i) {
       return P.part + (static_cast<size_t>(i) * 2 + (i == begin ? 1 : 0)) * S::kPart;
     };
@@ -610,18 +619,34 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : sizeof(T) == 4 ? 1 : 2
       const int at = (threadIdx.x + k * kConsumers * 32) * 4;
       const int row = at / HD, ch = at % HD;
       if (row >= mc) continue;
-      float mx = kFloor;
-      for (int i = begin; i <= end; ++i) mx = fmaxf(mx, __ldcg(part_of(i) + RT * HD + row));
-      float sum = 0.f;
+      // eight parts' loads at a time; the running maximum and sums as in a softmax
+      float mx = kFloor, sum = 0.f;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int i = begin; i <= end; ++i) {
-        const float* p = part_of(i);
-        const float fac = ex2_approx(__ldcg(p + RT * HD + row) - mx);
-        const float4 a = __ldcg(reinterpret_cast<const float4*>(p + row * HD + ch));
-        sum = fmaf(__ldcg(p + RT * HD + RT + row), fac, sum);
-        v.x = fmaf(a.x, fac, v.x); v.y = fmaf(a.y, fac, v.y);
-        v.z = fmaf(a.z, fac, v.z); v.w = fmaf(a.w, fac, v.w);
+      constexpr int kBatch = 8;
+      for (int i0 = begin; i0 <= end; i0 += kBatch) {
+        float pm[kBatch], ps[kBatch];
+        float4 pv[kBatch];
+#pragma unroll
+        for (int y = 0; y < kBatch; ++y) {
+          const float* p = part_of(min(i0 + y, end));
+          pm[y] = __ldcg(p + RT * HD + row);
+          ps[y] = __ldcg(p + RT * HD + RT + row);
+          pv[y] = __ldcg(reinterpret_cast<const float4*>(p + row * HD + ch));
+        }
+        float top = mx;
+#pragma unroll
+        for (int y = 0; y < kBatch; ++y) top = fmaxf(top, pm[y]);
+        const float old = ex2_approx(mx - top);
+        sum *= old;
+        v.x *= old; v.y *= old; v.z *= old; v.w *= old;
+        mx = top;
+#pragma unroll
+        for (int y = 0; y < kBatch; ++y) {
+          const float fac = i0 + y <= end ? ex2_approx(pm[y] - mx) : 0.f;
+          sum = fmaf(ps[y], fac, sum);
+          v.x = fmaf(pv[y].x, fac, v.x); v.y = fmaf(pv[y].y, fac, v.y);
+          v.z = fmaf(pv[y].z, fac, v.z); v.w = fmaf(pv[y].w, fac, v.w);
+        }
       }
       finish(row, ch, v, mx, sum);
     }

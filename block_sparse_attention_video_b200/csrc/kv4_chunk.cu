@@ -129,8 +129,7 @@ __device__ void produce(const AttnParams& P, Smem<HD>& sm) {
       int steps;
       if (x == lo) {
         steps = max(1, en.steps(entry, b, m0, seen, &m));
-        which = static_cast<int>(sm.piece.rem / steps);
-        m.s0 = static_cast<int>(sm.piece.rem - static_cast<long long>(which) * steps);
+        which = static_cast<int>(divide(sm.piece.rem, steps, m.s0));
       } else {
         if (++which == mult) {
           which = 0;
@@ -564,20 +563,19 @@ __device__ void softmax(const AttnParams& P, Smem<HD>& sm, uint32_t tmem) {
       mine[HD * 128 + 128 + row] = l_run;
     }
     tc_fence_before();
-    __threadfence();
     auto meet = [&]() -> bool {
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.meet[X]);
       return wait(&sm.meet[X], met++ & 1);
     };
     if (!meet()) return;
-    if (row == 0) {
+    if (row == 0) {   // one thread's fences, between the barriers, cover the slot's stores and loads
+      __threadfence();
       sm.joiner[X] = atomicAdd(P.arrived + begin * 2 + X, 1) == end - begin;
       __threadfence();
     }
     if (!meet()) return;
     if (!sm.joiner[X]) continue;
-    __threadfence();
     float mx = kFloor, sum = 0.f;
     for (int i = begin; i <= end; ++i) mx = fmaxf(mx, __ldcg(part_of(i) + HD * 128 + row));
     for (int i = begin; i <= end; ++i) {

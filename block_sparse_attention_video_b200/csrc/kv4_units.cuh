@@ -65,6 +65,18 @@ struct Seqs {
   }
 };
 
+// a / b and the remainder for a >= 0, b > 0: 32-bit where both fit.
+__device__ __forceinline__ long long divide(long long a, int b, int& rest) {
+  if (a <= 0xFFFFFFFFll) {
+    const unsigned q = static_cast<unsigned>(a) / static_cast<unsigned>(b);
+    rest = static_cast<int>(static_cast<unsigned>(a) - q * b);
+    return q;
+  }
+  const long long q = a / b;
+  rest = static_cast<int>(a - q * b);
+  return q;
+}
+
 // Entries are what the units are counted by: without lists, tiles of RT pairs of a
 // sequence (each counts for all KV heads); with lists, (row, KV head) (each counts for
 // all tiles of its query heads). Tiles are numbered without a prefix sum: sequence b owns
@@ -85,7 +97,8 @@ struct Entries {
   __device__ int steps(long long e, int& b, int& m0, int& seen, Meta* m) const {
     if (P.kv_idx) {
       int cnt = __ldg(P.kv_cnt + e);
-      const int r = static_cast<int>(e / P.c.H);
+      int h;
+      const int r = static_cast<int>(divide(e, P.c.H, h));
       if (r >= cu[P.bt.B]) return 0;
       int lo = 0, hi = P.bt.B;                  // cu[lo] <= r < cu[hi]
       while (hi - lo > 1) {
@@ -190,9 +203,16 @@ __device__ void find_piece(const AttnParams& P, Seqs& seqs, Piece& sm, int least
   __syncthreads();
 }
 
-// Block that holds position x of the line: the last i with total i / blocks <= x.
+// Block that holds position x of the line: the largest i with floor(total i / blocks) <= x,
+// that is total i < (x + 1) blocks. An estimate, corrected with products: 64-bit divisions
+// cost hundreds of cycles here.
 __device__ __forceinline__ int piece_of(long long x, long long total, int blocks) {
-  return static_cast<int>(((x + 1) * blocks - 1) / total);
+  const long long limit = (x + 1) * blocks;
+  int i = static_cast<int>(static_cast<float>(x) * (static_cast<float>(blocks) / static_cast<float>(total)));
+  i = min(max(i, 0), blocks - 1);
+  while (i > 0 && total * i >= limit) --i;
+  while (i + 1 < blocks && total * (i + 1) < limit) ++i;
+  return i;
 }
 
 }  // namespace kv4
