@@ -82,10 +82,16 @@ size_t pool_bytes(const fvattn_kv4_cache* c) {
   return static_cast<size_t>(c->num_pages) * c->H * c->block * (c->d + c->d / 8);
 }
 
-// Workspace check, and the header (and `clear` bytes behind it) cleared on the stream.
+__global__ void clear_kernel(uint4* p, int n) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) p[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// Workspace check, and the header (and `clear` bytes behind it) cleared on the stream: by a kernel,
+// because a memset between two kernels costs 3.0 us of the stream here and this 0.8 us.
 fvattn_status begin(void* ws, size_t have, size_t need, cudaStream_t st, size_t clear = 0) {
   if (!ws || !aligned(ws, 256) || have < need) return FVATTN_ERR_WORKSPACE;
-  return cudaMemsetAsync(ws, 0, kWsHeaderBytes + clear, st) == cudaSuccess ? FVATTN_OK : FVATTN_ERR_CUDA;
+  clear_kernel<<<1, 128, 0, st>>>(static_cast<uint4*>(ws), static_cast<int>((kWsHeaderBytes + clear) / 16));
+  return cudaGetLastError() == cudaSuccess ? FVATTN_OK : FVATTN_ERR_CUDA;
 }
 
 // SM count of the current device, kept after the first look-up (every writer of an entry stores
