@@ -209,7 +209,8 @@ fvattn_status fvattn_kv4_attn(const fvattn_kv4_cache* cache, const fvattn_kv4_ba
   const int es = dtype == FVATTN_BF16 ? 2 : 4;
   bool ok;
   const size_t nq = strided_bytes(batch->rows, Hq, cache->d, q_stride, es, &ok);
-  if (!ok || overlap(q, nq, out, static_cast<size_t>(batch->rows) * Hq * cache->d * es)) return FVATTN_ERR_INVALID_ARG;
+  const size_t no = static_cast<size_t>(batch->rows) * Hq * cache->d * es;
+  if (!ok || overlap(q, nq, out, no) || overlap(out, no, cache->pages, pool_bytes(cache))) return FVATTN_ERR_INVALID_ARG;
   const size_t need = fvattn_kv4_workspace_bytes(FVATTN_OP_KV4_ATTN, cache, batch, Hq);
   auto st = static_cast<cudaStream_t>(stream);
   const fvattn_status s = begin(workspace, workspace_bytes, need, st, fvattn::kv4::attn_ws_clear());

@@ -238,8 +238,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : sizeof(T) == 4 ? 1 : 2
   if (len <= 0) return;
   if (warp == kConsumers) {
     produce<HD, NT>(P, sm);
-    if (blockIdx.x == 0 && (threadIdx.x & 31) == 0 && __ldg(P.bt.cu + P.bt.B) > P.bt.rows)
-      record_status(P.status, FVATTN_ERR_INVALID_ARG);
     return;
   }
 
@@ -660,8 +658,10 @@ constexpr int kMaxChunkBlocks = 160;
 size_t chunk_part_bytes(int d, int grid);
 cudaError_t launch_chunk(const AttnParams& P, int d, int grid, cudaStream_t st);
 
-// Where the tensor cores' 128-row tiles take over (the fp32 path and lists stay here).
-static bool many_rows(int max_q, int G) { return static_cast<long long>(max_q) * G > 16; }
+// Where the 128-row tiles of kv4_chunk.cu take over (the fp32 path and lists stay here). Measured
+// at d 128, 8 KV heads, 16 sequences of up to 16k: 20 rows 286 us here and 307 there, 40 rows
+// 411 and 314; one sequence of 32k, 12 heads: 17 rows 62 and 83, 40 rows 91 and 86.
+static bool many_rows(int max_q, int G) { return static_cast<long long>(max_q) * G > 32; }
 
 // Bytes behind the header that a call clears.
 size_t attn_ws_clear() { return align_up(kMaxBlocks * sizeof(int), 256); }

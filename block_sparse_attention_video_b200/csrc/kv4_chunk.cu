@@ -637,7 +637,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const AttnParam
     mbar_init(&sm.mma_done, 1);
     sm.abort_flag = 0;
     fence_mbarrier_init();
-    if (blockIdx.x == 0 && __ldg(P.bt.cu + P.bt.B) > P.bt.rows) record_status(P.status, FVATTN_ERR_INVALID_ARG);
   }
   // A unit's own costs (Q, epilogue) are about three steps'.
   find_piece<kRows, kThreads>(P, sm.seqs, sm.piece, 4);

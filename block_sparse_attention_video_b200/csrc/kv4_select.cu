@@ -293,7 +293,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
   const int b = lo, r0 = cu[b], r1 = cu[b + 1];
   const int first = r0 + (tile - (r0 / RU + b)) * RU;                // first row of the group
   const int rows = min(RU, min(r1, P.bt.rows) - first);
-  if (first < r0 || rows <= 0) return;
+  if (r0 < 0 && tid == 0) record_status(P.status, FVATTN_ERR_INVALID_ARG);
+  if (r0 < 0 || first < r0 || rows <= 0) return;
   const int n = held(kv_len[b], P.bt, P.block, P.status);
   const int pos0 = n - (r1 - first);                                 // position of the first row
   const int most = pos0 + rows - 1 < 0 ? 0 : (pos0 + rows - 1) / P.block;   // pages to score

@@ -106,6 +106,7 @@ struct Entries {
         if (cu[mid] <= r) lo = mid; else hi = mid;
       }
       b = lo;
+      if (r < cu[b]) return 0;                  // before the first sequence
       if (cnt < 0 || cnt > P.bt.max_pages) {
         record_status(P.status, FVATTN_ERR_INVALID_ARG);
         cnt = min(max(cnt, 0), P.bt.max_pages);
@@ -129,7 +130,8 @@ struct Entries {
     const int r0 = cu[b], r1 = cu[b + 1];
     const int q = min(r1, P.bt.rows) - r0;
     const long long first = (e - (static_cast<long long>(r0) * P.G / RT + b)) * RT;
-    if (q <= 0 || first >= static_cast<long long>(q) * P.G) return 0;
+    if (r0 < 0) record_status(P.status, FVATTN_ERR_INVALID_ARG);
+    if (r0 < 0 || q <= 0 || first < 0 || first >= static_cast<long long>(q) * P.G) return 0;
     m0 = static_cast<int>(first);
     const int n = held(kv_len[b], P.bt, P.block, P.status);
     const int last = min((m0 + RT - 1) / P.G, q - 1);
@@ -157,6 +159,7 @@ __device__ void find_piece(const AttnParams& P, Seqs& seqs, Piece& sm, int least
   seqs.load<kThreads>(P.bt);
   __syncthreads();
   const Entries<RT> en(P, seqs);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && en.cu[P.bt.B] > P.bt.rows) record_status(P.status, FVATTN_ERR_INVALID_ARG);
   const long long E = en.count();
   const int mult = en.times();
   const long long chunk = (E + kThreads - 1) / kThreads;

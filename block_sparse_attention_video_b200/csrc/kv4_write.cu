@@ -167,7 +167,8 @@ __global__ void __launch_bounds__(kWriteThreads, sizeof(T) == 2 ? 4 : 3)
   const int b = lo;
   const int r0 = cu[b];
   const int q = cu[b + 1] - r0;
-  if (q <= 0) return;
+  if (r0 < 0 && threadIdx.x == 0) record_status(status, FVATTN_ERR_INVALID_ARG);
+  if (q <= 0 || r0 < 0) return;
   const int n = held(kv_len[b], bt, block, status);
   const int start = n - q;                    // position of row r0
   if (start < 0 && threadIdx.x == 0) record_status(status, FVATTN_ERR_INVALID_ARG);
@@ -276,11 +277,14 @@ __global__ void __launch_bounds__(kWriteThreads)
         const int mid = (lo + hi) >> 1;
         if (cu[mid] <= r) lo = mid; else hi = mid;
       }
-      const int b = lo, n = held(kv_len[b], bt, block, status), pos = n - (cu[b + 1] - r);
-      slot = -1;
-      if (pos >= 0 && pos < n) slot = pool_slot(bt, c.num_pages, b, pos / block, status);
-      else record_status(status, FVATTN_ERR_INVALID_ARG);
-      t = pos >= 0 ? pos % block : 0;
+      const int b = lo;
+      if (r >= cu[b]) {
+        const int n = held(kv_len[b], bt, block, status), pos = n - (cu[b + 1] - r);
+        slot = -1;
+        if (pos >= 0 && pos < n) slot = pool_slot(bt, c.num_pages, b, pos / block, status);
+        else record_status(status, FVATTN_ERR_INVALID_ARG);
+        t = pos >= 0 ? pos % block : 0;
+      }
     }
     place[i] = make_int2(slot, t);
   }

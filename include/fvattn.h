@@ -431,7 +431,7 @@ typedef struct {
  * All three arrays are device memory and are read when the call's kernels run, so lengths
  * may change between the replays of a captured call. What they hold is checked there, each
  * element where it is used: a position outside [0, max_pages*block), a pool slot outside
- * [0, num_pages) or cu[B] > rows is skipped or clamped and recorded as
+ * [0, num_pages), cu[b] < 0 or cu[B] > rows is skipped or clamped and recorded as
  * FVATTN_ERR_INVALID_ARG in the workspace. A sequence may have no rows. Two sequences may
  * share pages that no row of the call writes.                                           */
 typedef struct {
@@ -491,7 +491,7 @@ FVATTN_API fvattn_status fvattn_kv4_select(const fvattn_kv4_cache* cache, const 
                                            void* stream);
 
 /* Attention of the call's rows over the cache. q [rows, Hq, d] with q_stride elements from
- * row to row, out [rows, Hq, d] dense, both of dtype; q and out must not overlap. Query head h
+ * row to row, out [rows, Hq, d] dense, both of dtype; out overlaps neither q nor the pages. Query head h
  * reads KV head h / (Hq/H). A row at position t sees the tokens at positions <= t (causal != 0) or all
  * kv_len of its sequence (causal == 0), and with lists only those in the pages
  * kv_idx[row, h, 0..kv_cnt) (layout of fvattn_kv4_select). out = softmax(scale * q . k) . v over the

@@ -101,6 +101,11 @@ class Case:
             out.append(np.stack((x & 15, x >> 4), -1).reshape(*x.shape[:3], -1) if i % 2 == 0 else x)
         return out
 
+    def assert_records(self, want):
+        """The pool's records equal ``want`` (an earlier ``records()``), a zero's sign aside."""
+        for i, (g, w) in enumerate(zip(self.records(), want)):
+            assert np.all((g == w) | (((g & 7) == 0) & ((w & 7) == 0)) if i % 2 == 0 else g == w)
+
     def make_q(self, dtype=None, spread=1.0, pad=0):
         q = spread * torch.randn((self.rows + pad, self.Hq, self.d), generator=self.g)
         return q.to(dtype or self.dtype)
@@ -594,6 +599,139 @@ def test_writes_outside_the_table_are_refused_on_the_device():
     F.fvattn_kv4_read(c.cache, b, ko, vo, ws)
     assert F.fvattn_workspace_status(ws) == F.FVATTN_ERR_INVALID_ARG
     assert not ko[:6].any() and ko[6:].abs().sum() > 0
+
+
+# ------------------------------------------------------------------ many sequences, long tables, odd batches
+def test_more_sequences_than_shared_memory_holds():
+    """300 sequences: all four calls search the lengths in global memory then."""
+    g = torch.Generator().manual_seed(40)
+    kv = torch.randint(0, 150, (300,), generator=g).tolist()
+    rows = [min(n, i % 3) for i, n in enumerate(kv)]
+    c = Case(kv, rows, 1, 64, 64, seed=41, Hq=3)
+    q = c.make_q(spread=4.0)
+    idx, cnt = _select(c, q, 0.6, 1)
+    want = _want_lists(c, q, 0.6, 1)
+    assert [idx[r, 0, :cnt[r, 0]].tolist() for r in range(c.rows)] == [w[0] for w in want]
+    out, lse = c.attend(q)
+    c.check(q, out, lse, rows=set(range(0, c.rows, 13)))
+    out, lse = c.attend(q, True, idx, cnt)
+    c.check(q, out, lse, lists=want, rows=set(range(0, c.rows, 17)))
+    many = c.batch_of([min(n, 40) for n in kv])
+    n = sum(min(x, 40) for x in kv)
+    ko, vo = (torch.empty((n, 1, 64), device="cuda") for _ in range(2))
+    F.fvattn_kv4_read(c.cache, many, ko, vo, c.ws(F.FVATTN_OP_KV4_READ, n, many))
+    r = 0
+    for i, x in enumerate(kv):
+        m = min(x, 40)
+        if m and i % 11 == 0:
+            k, v = c.values(i)
+            assert np.array_equal(ko[r:r + m].cpu().numpy(), k[x - m:]) and np.array_equal(vo[r:r + m].cpu().numpy(), v[x - m:])
+        r += m
+
+
+@pytest.mark.parametrize("Hq,kv,p", [(8, 190_000, 0.9), (1, 70_000, 0.95), (3, 70_000, 0.5)])
+def test_selection_over_many_pages(Hq, kv, p):
+    """Up to 2,968 pages; with eight heads shared memory holds four at a time."""
+    c = Case([kv], [1], 1, 64, 64, seed=42, Hq=Hq)
+    q = c.make_q(spread=3.0)
+    idx, cnt = _select(c, q, p, 2)
+    want = _want_lists(c, q, p, 2)[0][0]
+    assert idx[0, 0, :cnt[0, 0]].tolist() == want
+
+
+def test_widest_table():
+    c = Case([1000], [2], 2, 64, 64, seed=43, Hq=6)
+    q = c.make_q(spread=4.0)
+    want = _want_lists(c, q, 0.8, 1)
+    wide = torch.zeros((1, 8192), dtype=torch.int32, device="cuda")
+    wide[0, :c.max_pages] = c.table[0].clamp(min=0)
+    c.table, c.max_pages = wide, 8192
+    c.batch = c.batch_of([2])
+    idx, cnt = _select(c, q, 0.8, 1)
+    assert [[idx[r, h, :cnt[r, h]].tolist() for h in range(2)] for r in range(2)] == want
+    out, lse = c.attend(q, True, idx, cnt)
+    c.check(q, out, lse, lists=want)
+
+
+@pytest.mark.parametrize("p,k_min", [(0.55, 1), (0.1, 40), (0.999, 1)])
+def test_equal_masses(p, k_min):
+    """q = 0: more pages tie than the quick search takes; they go in index order."""
+    c = Case([64 * 100 + 9], [1], 1, 64, 64, seed=44, Hq=2)
+    q = torch.zeros((1, 2, 64), dtype=BF16)
+    idx, cnt = _select(c, q, p, k_min)
+    assert idx[0, 0, :cnt[0, 0]].tolist() == _want_lists(c, q, p, k_min)[0][0]
+
+
+def test_one_sharp_page_and_a_long_tail():
+    """Masses over hundreds of binades, down to 0."""
+    c = Case([64 * 400 + 1], [1], 1, 64, 64, seed=45, Hq=1)
+    q = c.make_q(spread=300.0)
+    for p, k_min in ((0.5, 1), (0.9999, 1), (0.5, 60)):
+        idx, cnt = _select(c, q, p, k_min)
+        assert idx[0, 0, :cnt[0, 0]].tolist() == _want_lists(c, q, p, k_min)[0][0]
+
+
+@pytest.mark.parametrize("claimed", [1, 500])
+def test_max_q_only_chooses_the_kernel(claimed):
+    c = Case([400, 130], [60, 1], 1, 64, 64, seed=46, Hq=2)
+    c.batch = F.KV4Batch(c.table, c.batch.kv_len, c.batch.cu, claimed)
+    q = c.make_q()
+    out, lse = c.attend(q)
+    assert F.fvattn_workspace_status(c.last_ws) == F.FVATTN_OK
+    c.check(q, out, lse, rows=set(range(0, 61, 7)) | {60})
+
+
+@pytest.mark.parametrize("rows", [[3, 1], [100, 40]])
+def test_a_bad_row_leaves_the_others(rows):
+    c = Case([300, 200], rows, 1, 128, 64, seed=47, Hq=4)
+    q = c.make_q()
+    good, gl = c.attend(q)
+    q[1, 2, 5], q[2, 0, 0] = math.nan, math.inf
+    out, lse = c.attend(q)
+    keep = torch.ones(q.shape[:2], dtype=torch.bool)
+    keep[1, 2] = keep[2, 0] = False
+    assert torch.equal(out[keep], good[keep]) and torch.equal(lse[keep], gl[keep])
+    assert out[1, 2].isnan().all() and out[2, 0].isnan().all()
+
+
+@pytest.mark.parametrize("cu", [[2, 4, 5], [-3, 1, 2], [0, 4, 2], [0, 3, 900]])
+def test_odd_row_starts(cu):
+    """Rows before cu[0] belong to no sequence; a negative, falling or too large start is skipped and recorded."""
+    c = Case([300, 200], [2, 1], 1, 64, 64, seed=48, Hq=2)
+    cut = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    n = 6
+    q = torch.randn((n, 2, 64), generator=c.g).to(BF16).cuda()
+    for max_q in (1, 300):
+        c.batch = F.KV4Batch(c.table, c.batch.kv_len, cut, max_q)
+        out, lse = c.attend(q)
+        bad = F.fvattn_workspace_status(c.last_ws)
+        assert bad == (F.FVATTN_OK if cu in ([2, 4, 5], [0, 4, 2]) else F.FVATTN_ERR_INVALID_ARG)
+        if cu[0] == 2:
+            assert torch.all(out[:2] == 77) and torch.all(out[5:] == 77) and torch.isfinite(out).all()
+            c.nrow, c.kv = [2, 1], [300, 200]
+            c.check(q[2:].cpu(), out[2:], lse[2:])
+    idx, cnt = _select(c, q.cpu(), 0.9, 1)
+    before = c.records()
+    ko, vo = (torch.full((n, 1, 64), 5.0, device="cuda") for _ in range(2))
+    F.fvattn_kv4_read(c.cache, c.batch, ko, vo, c.ws(F.FVATTN_OP_KV4_READ, n))
+    if cu[0] == 2:
+        assert torch.all(cnt[:2] == -5) and torch.all(cnt[2:5] > 0) and torch.all(cnt[5:] == -5)
+        assert torch.all(ko[:2] == 5) and torch.all(ko[5:] == 5)
+        F.fvattn_kv4_append(c.cache, c.batch, ko, vo, c.ws(F.FVATTN_OP_KV4_APPEND, n))
+        c.assert_records(before)                            # what was read is what is written again
+
+
+def test_rewriting_what_was_read_changes_nothing():
+    """Quantizing stored values gives them back: codes, scales and sums."""
+    c = Case([200, 130], [200, 130], 2, 128, 64, seed=49)
+    before, sums = c.records(), c.cache.ksum.clone()
+    ko, vo = (torch.empty((330, 2, 128), device="cuda") for _ in range(2))
+    F.fvattn_kv4_read(c.cache, c.batch, ko, vo, c.ws(F.FVATTN_OP_KV4_READ, 330))
+    F.fvattn_kv4_append(c.cache, c.batch, ko, vo, c.ws(F.FVATTN_OP_KV4_APPEND, 330))
+    # (a group's largest stored magnitude is 6 scales, so its scale comes out the same)
+    full = [int(c.table_np[i, p]) for i, n in enumerate(c.kv) for p in range(n // 64)]
+    c.assert_records(before)
+    assert torch.equal(sums[full], c.cache.ksum[full])
 
 
 # ------------------------------------------------------------------ together, streams, graphs, refusals
