@@ -179,6 +179,7 @@ def _ptr(t):
 def _stream(stream, device=None):
     """The given stream (which must belong to ``device``), else ``device``'s current stream."""
     if stream is None:
+        # (an index spares torch a lookup; this runs at every call)
         s = torch.cuda.current_stream(device if device is None else torch.device(device).index)
     else:
         s = stream

@@ -60,10 +60,11 @@ __device__ __forceinline__ double sort32(double v) {
   return v;
 }
 
-// What the search of a row's cut finds: the mass v* and the number of pages selected.
+// What the search of a row's cut finds: the mass v*, the number of pages selected and of those
+// above v*.
 struct Cut {
   double star;
-  int cnt;
+  int cnt, above;
 };
 
 // The cut among at most 32 masses, one a lane, v descending: those above them number c_hi and
@@ -81,6 +82,7 @@ __device__ __forceinline__ bool cut_sorted(double v, int in, int c_hi, double f_
   const int at = __ffs(reach) - 1;
   cut.star = __shfl_sync(0xffffffffu, v, at);
   cut.cnt = c_hi + at + 1;
+  cut.above = c_hi + __popc(__ballot_sync(0xffffffffu, v > cut.star));
   return true;
 }
 
@@ -201,6 +203,7 @@ __device__ bool full_cut(const double* x, int n, double target, bool by_count, i
     double acc = f_hi + cut.star;
     while (acc < target && need < c_lo - c_hi) { acc += cut.star; ++need; }
     cut.cnt = by_count ? want : c_hi + need;
+    cut.above = c_hi;
     return true;
   }
   int have = 0;
@@ -213,6 +216,7 @@ __device__ bool full_cut(const double* x, int n, double target, bool by_count, i
   if (by_count) {
     cut.star = __shfl_sync(0xffffffffu, v, want - c_hi - 1);
     cut.cnt = want;
+    cut.above = c_hi + __popc(__ballot_sync(0xffffffffu, v > cut.star));
     return true;
   }
   return cut_sorted(v, have, c_hi, f_hi, target, cut);
@@ -233,12 +237,7 @@ __device__ void pick_pages(const double* x, const float* f, int n, float p, int 
     if (found && cut.cnt < k_min) full_cut(x, n, 2.0, true, k_min, box, cut);   // the floor
   }
   // all pages above v*, and at v* the first ones that fill the count
-  int above = 0;
-  if (!all) {
-    for (int j = lane; j < n; j += 32) above += x[j] > cut.star;
-    above = __reduce_add_sync(0xffffffffu, above);
-  }
-  const int take = all ? 0 : cut.cnt - above;
+  const int take = all ? 0 : cut.cnt - cut.above;
   int written = 0, tied = 0;
   for (int j0 = 0; j0 < n; j0 += 32) {
     const int j = j0 + lane;
