@@ -176,11 +176,17 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# The current stream's handle without a Stream object around it (2 us less at every call), where
+# this torch has the call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, device=None):
     """The given stream (which must belong to ``device``), else ``device``'s current stream."""
     if stream is None:
-        # (an index spares torch a lookup; this runs at every call)
-        s = torch.cuda.current_stream(device if device is None else torch.device(device).index)
+        if _raw_stream is not None and device is not None and device.index is not None:
+            return _raw_stream(device.index)
+        s = torch.cuda.current_stream(device)
     else:
         s = stream
         if device is not None and s.device != torch.device(device):
@@ -204,7 +210,7 @@ def _expect(t, name, dev, shape=None, dtype=None, optional=False):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
