@@ -77,6 +77,12 @@ struct Divisor {
   }
 };
 
+// Two products, and two quotients corrected once: q + r (x - q y) of q = x r. The packed
+// operations take one issue slot for two values; issue slots are what bounds the kernel next.
+__device__ __forceinline__ float2 corrected2(float2 x, float2 q, float2 minus_y, float2 r) {
+  return __ffma2_rn(__ffma2_rn(q, minus_y, x), r, q);
+}
+
 __device__ __forceinline__ float reciprocal(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -103,8 +109,16 @@ __device__ __forceinline__ uint32_t quantize8(const Raw8<T>& raw, const Divisor&
   }
   if (head.kind == 1) {   // division is monotonic: the largest quotient is the largest's
     m = head.corrected(m);
+    const float2 r2 = make_float2(head.r, head.r), y2 = make_float2(-head.y, -head.y);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = head.corrected(x[i]);
+    for (int i = 0; i < 8; i += 2) {
+      const float2 v = make_float2(x[i], x[i + 1]);
+      float2 q = __fmul2_rn(v, r2);
+      q = corrected2(v, q, y2, r2);
+      q = corrected2(v, q, y2, r2);
+      x[i] = q.x;
+      x[i + 1] = q.y;
+    }
   } else if (head.kind == 2) {
     m = m / head.y;
 #pragma unroll
@@ -115,11 +129,14 @@ __device__ __forceinline__ uint32_t quantize8(const Raw8<T>& raw, const Divisor&
   scale = float_to_e4m3(fminf(c, 448.f));     // 448 where an infinite m has made c a NaN
   const float s = e4m3_to_float(scale);
   const float r = scale == 0u ? 0.f : reciprocal(s);   // codes 0 where the scale is
+  const float2 r2 = make_float2(r, r), s2 = make_float2(-s, -s);
   float q[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float q0 = x[i] * r;
-    q[i] = fmaf(fmaf(-q0, s, x[i]), r, q0);
+  for (int i = 0; i < 8; i += 2) {
+    const float2 v = make_float2(x[i], x[i + 1]);
+    const float2 d = corrected2(v, __fmul2_rn(v, r2), s2, r2);
+    q[i] = d.x;
+    q[i + 1] = d.y;
   }
   return pack_e2m1x8(q);
 }
@@ -132,11 +149,12 @@ __device__ __forceinline__ void add8(uint32_t codes, uint32_t scale, uint32_t (&
   uint32_t p[4];
   e2m1x8_to_half2(codes, p);
   const float s = e4m3_to_float(scale) * 1024.f;
+  const float2 s2 = make_float2(s, s), magic = make_float2(12582912.f, 12582912.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
-    acc[2 * i] += __float_as_uint(fmaf(f.x, s, 12582912.f));
-    acc[2 * i + 1] += __float_as_uint(fmaf(f.y, s, 12582912.f));
+    const float2 f = __ffma2_rn(__half22float2(*reinterpret_cast<const __half2*>(&p[i])), s2, magic);
+    acc[2 * i] += __float_as_uint(f.x);
+    acc[2 * i + 1] += __float_as_uint(f.y);
   }
 }
 
