@@ -562,12 +562,14 @@ fvattn_status fvattn_wait_selftest(int64_t* results, void* workspace, size_t wor
 
 fvattn_status fvattn_workspace_status(const void* workspace, void* stream) {
   if (!workspace || !aligned(workspace, 256)) return FVATTN_ERR_WORKSPACE;
-  int h = 0;
+  fvattn::WsHeader h;
   auto st = static_cast<cudaStream_t>(stream);
-  if (cudaMemcpyAsync(&h, workspace, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess)
+  if (cudaMemcpyAsync(&h, workspace, sizeof(h), cudaMemcpyDeviceToHost, st) != cudaSuccess)
     return FVATTN_ERR_CUDA;
   if (cudaStreamSynchronize(st) != cudaSuccess) return FVATTN_ERR_CUDA;
-  return static_cast<fvattn_status>(h);
+  // a call that numbers itself left its number, and any error under it; the others a plain word
+  if (h.call != 0ull) return h.record >> 8 == h.call ? static_cast<fvattn_status>(h.record & 0xFFu) : FVATTN_OK;
+  return static_cast<fvattn_status>(h.status);
 }
 
 const char* fvattn_status_string(fvattn_status s) {

@@ -15,7 +15,11 @@ struct WsHeader {
   int status;                  // first error recorded by a kernel (0 = none)
   int pad0;
   unsigned long long counter;  // dynamic work-unit counter of the attention scheduler
-  unsigned long long pad[30];
+  // The 4-bit cache's calls: the number of the last call (0 after any other call, which clears
+  // the header) and the first error recorded, call << 8 | status, of whatever call it was.
+  unsigned long long call;
+  unsigned long long record;
+  unsigned long long pad[28];
 };
 static_assert(sizeof(WsHeader) == 256, "workspace header must be 256 bytes");
 constexpr size_t kWsHeaderBytes = 256;

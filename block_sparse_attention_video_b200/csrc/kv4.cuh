@@ -36,8 +36,43 @@ struct Batch {
   int B, max_pages, rows;
 };
 
+// Where a call's kernels record errors. Every call has a number of its own, so nothing has to be
+// cleared before it: what other calls have left in the workspace does not carry its number.
+// (Replays of a captured call share theirs; there a kernel clears the words first.)
+struct Status {
+  WsHeader* h;
+  unsigned long long call;   // 1 .. 2^48 - 1
+};
+
+// Names the call in the workspace; by one thread of the grid.
+__device__ __forceinline__ void open_call(const Status& s) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) s.h->call = s.call;
+}
+
+// The call's first error stays.
+__device__ __forceinline__ void record_status(const Status& s, int code) {
+  unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(&s.h->record);
+  while ((old >> 8) != s.call) {
+    const unsigned long long seen = atomicCAS(&s.h->record, old, s.call << 8 | static_cast<unsigned>(code));
+    if (seen == old) return;
+    old = seen;
+  }
+}
+
+// Arrival at a counter that need not be cleared either: call << 16 | arrivals. Returns how many
+// of this call came before.
+__device__ __forceinline__ int arrive_at(unsigned long long* word, unsigned long long call) {
+  unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(word);
+  while (true) {
+    const unsigned long long base = (old >> 16) == call ? old : call << 16;
+    const unsigned long long seen = atomicCAS(word, old, base + 1);
+    if (seen == old) return static_cast<int>(base & 0xFFFFu);
+    old = seen;
+  }
+}
+
 // A sequence's length n, clamped to what its table row can hold.
-__device__ __forceinline__ int held(int n, const Batch& bt, int block, int* status) {
+__device__ __forceinline__ int held(int n, const Batch& bt, int block, const Status& status) {
   const int most = bt.max_pages * block;
   if (n < 0 || n > most) {
     record_status(status, FVATTN_ERR_INVALID_ARG);
@@ -47,7 +82,7 @@ __device__ __forceinline__ int held(int n, const Batch& bt, int block, int* stat
 }
 
 // Pool slot of page pg (in [0, max_pages)) of sequence b; -1 (recorded) if invalid.
-__device__ __forceinline__ int pool_slot(const Batch& bt, int num_pages, int b, int pg, int* status) {
+__device__ __forceinline__ int pool_slot(const Batch& bt, int num_pages, int b, int pg, const Status& status) {
   const int s = __ldg(bt.table + static_cast<size_t>(b) * bt.max_pages + pg);
   if (s < 0 || s >= num_pages) {
     record_status(status, FVATTN_ERR_INVALID_ARG);

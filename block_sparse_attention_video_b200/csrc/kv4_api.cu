@@ -9,15 +9,15 @@
 namespace fvattn {
 namespace kv4 {
 cudaError_t launch_append(const Cache& c, const Batch& bt, const void* k, const void* v, long long ks,
-                          long long vs, bool bf16, int d, int block, int* status, cudaStream_t st);
+                          long long vs, bool bf16, int d, int block, const Status& status, cudaStream_t st);
 cudaError_t launch_read(const Cache& c, const Batch& bt, void* k, void* v, bool bf16, int d, int block,
-                        int* status, cudaStream_t st);
+                        const Status& status, cudaStream_t st);
 cudaError_t launch_select(const Cache& c, const Batch& bt, const void* q, long long q_stride, int Hq, bool bf16,
                           float scale, float p, int k_min, int d, int block, int* kv_idx, int* kv_cnt,
-                          int* status, cudaStream_t st);
+                          const Status& status, cudaStream_t st);
 cudaError_t launch_attn(const Cache& c, const Batch& bt, const void* q, long long q_stride, int Hq, void* out,
                         float* lse, bool bf16, float scale, int causal, int d, int block, int max_q, const int* kv_idx,
-                        const int* kv_cnt, int* status, uint8_t* ws, int num_sms, cudaStream_t st);
+                        const int* kv_cnt, const Status& status, uint8_t* ws, int num_sms, cudaStream_t st);
 size_t attn_ws_bytes(int d, int max_q, int G);
 size_t attn_ws_clear();
 }  // namespace kv4
@@ -86,10 +86,20 @@ __global__ void clear_kernel(uint4* p, int n) {
   for (int i = threadIdx.x; i < n; i += blockDim.x) p[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// Workspace check, and the header (and `clear` bytes behind it) cleared on the stream: by a kernel,
-// because a memset between two kernels costs 3.0 us of the stream here and this 0.8 us.
-fvattn_status begin(void* ws, size_t have, size_t need, cudaStream_t st, size_t clear = 0) {
+// Workspace check, and the call's number (kv4.cuh). The header and `clear` bytes of counters behind
+// it are cleared only where that does not do: in a captured call, whose replays share the number,
+// and in a call without rows, which runs no other kernel. A clearing launch costs 2 us of host time
+// and 1 us of the stream; it is a kernel because a memset between two kernels costs 3 us.
+fvattn_status begin(void* ws, size_t have, size_t need, cudaStream_t st, int rows, fvattn::kv4::Status* status,
+                    size_t clear = 0) {
   if (!ws || !aligned(ws, 256) || have < need) return FVATTN_ERR_WORKSPACE;
+  static std::atomic<unsigned long long> calls{0x5EED00000001ull};
+  status->h = static_cast<fvattn::WsHeader*>(ws);
+  status->call = calls.fetch_add(1, std::memory_order_relaxed) & 0xFFFFFFFFFFFFull;
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  const bool known = cudaStreamIsCapturing(st, &cap) == cudaSuccess;
+  if (!known) cudaGetLastError();
+  if (known && cap == cudaStreamCaptureStatusNone && rows > 0) return FVATTN_OK;
   clear_kernel<<<1, 128, 0, st>>>(static_cast<uint4*>(ws), static_cast<int>((kWsHeaderBytes + clear) / 16));
   return cudaGetLastError() == cudaSuccess ? FVATTN_OK : FVATTN_ERR_CUDA;
 }
@@ -146,11 +156,11 @@ fvattn_status fvattn_kv4_append(const fvattn_kv4_cache* cache, const fvattn_kv4_
   const size_t np = pool_bytes(cache);
   if (overlap(k, nk, cache->pages, np) || overlap(v, nv, cache->pages, np)) return FVATTN_ERR_INVALID_ARG;
   auto st = static_cast<cudaStream_t>(stream);
-  const fvattn_status s = begin(workspace, workspace_bytes, kWsHeaderBytes, st);
+  fvattn::kv4::Status status;
+  const fvattn_status s = begin(workspace, workspace_bytes, kWsHeaderBytes, st, batch->rows, &status);
   if (s != FVATTN_OK || batch->rows == 0) return s;
-  auto hdr = static_cast<fvattn::WsHeader*>(workspace);
   return from_cuda(fvattn::kv4::launch_append(cache_of(cache), batch_of(batch), k, v, k_stride, v_stride,
-                                              dtype == FVATTN_BF16, cache->d, cache->block, &hdr->status, st));
+                                              dtype == FVATTN_BF16, cache->d, cache->block, status, st));
 }
 
 fvattn_status fvattn_kv4_read(const fvattn_kv4_cache* cache, const fvattn_kv4_batch* batch, void* k_out,
@@ -165,11 +175,11 @@ fvattn_status fvattn_kv4_read(const fvattn_kv4_cache* cache, const fvattn_kv4_ba
   if (overlap(k_out, no, v_out, no) || overlap(k_out, no, cache->pages, np) || overlap(v_out, no, cache->pages, np))
     return FVATTN_ERR_INVALID_ARG;
   auto st = static_cast<cudaStream_t>(stream);
-  const fvattn_status s = begin(workspace, workspace_bytes, kWsHeaderBytes, st);
+  fvattn::kv4::Status status;
+  const fvattn_status s = begin(workspace, workspace_bytes, kWsHeaderBytes, st, batch->rows, &status);
   if (s != FVATTN_OK || batch->rows == 0) return s;
-  auto hdr = static_cast<fvattn::WsHeader*>(workspace);
   return from_cuda(fvattn::kv4::launch_read(cache_of(cache), batch_of(batch), k_out, v_out, dtype == FVATTN_BF16,
-                                            cache->d, cache->block, &hdr->status, st));
+                                            cache->d, cache->block, status, st));
 }
 
 fvattn_status fvattn_kv4_select(const fvattn_kv4_cache* cache, const fvattn_kv4_batch* batch, const void* q,
@@ -188,11 +198,11 @@ fvattn_status fvattn_kv4_select(const fvattn_kv4_cache* cache, const fvattn_kv4_
   if (!ok) return FVATTN_ERR_INVALID_ARG;
   const size_t need = fvattn_kv4_workspace_bytes(FVATTN_OP_KV4_SELECT, cache, batch, Hq);
   auto st = static_cast<cudaStream_t>(stream);
-  const fvattn_status s = begin(workspace, workspace_bytes, need, st);
+  fvattn::kv4::Status status;
+  const fvattn_status s = begin(workspace, workspace_bytes, need, st, batch->rows, &status);
   if (s != FVATTN_OK || batch->rows == 0) return s;
-  auto hdr = static_cast<fvattn::WsHeader*>(workspace);
   return from_cuda(fvattn::kv4::launch_select(cache_of(cache), batch_of(batch), q, q_stride, Hq,
-                                              dtype == FVATTN_BF16, scale, p, k_min, cache->d, cache->block, kv_idx, kv_cnt, &hdr->status, st));
+                                              dtype == FVATTN_BF16, scale, p, k_min, cache->d, cache->block, kv_idx, kv_cnt, status, st));
 }
 
 fvattn_status fvattn_kv4_attn(const fvattn_kv4_cache* cache, const fvattn_kv4_batch* batch, const void* q,
@@ -213,14 +223,15 @@ fvattn_status fvattn_kv4_attn(const fvattn_kv4_cache* cache, const fvattn_kv4_ba
   if (!ok || overlap(q, nq, out, no) || overlap(out, no, cache->pages, pool_bytes(cache))) return FVATTN_ERR_INVALID_ARG;
   const size_t need = fvattn_kv4_workspace_bytes(FVATTN_OP_KV4_ATTN, cache, batch, Hq);
   auto st = static_cast<cudaStream_t>(stream);
-  const fvattn_status s = begin(workspace, workspace_bytes, need, st, fvattn::kv4::attn_ws_clear());
+  fvattn::kv4::Status status;
+  const fvattn_status s = begin(workspace, workspace_bytes, need, st, batch->rows, &status,
+                                fvattn::kv4::attn_ws_clear());
   if (s != FVATTN_OK || batch->rows == 0) return s;
   const int sms = device_sm_count();
   if (sms <= 0) return FVATTN_ERR_CUDA;
-  auto hdr = static_cast<fvattn::WsHeader*>(workspace);
   return from_cuda(fvattn::kv4::launch_attn(cache_of(cache), batch_of(batch), q, q_stride, Hq, out, lse,
                                             dtype == FVATTN_BF16, scale, causal != 0, cache->d, cache->block,
-                                            batch->max_q, kv_idx, kv_cnt, &hdr->status,
+                                            batch->max_q, kv_idx, kv_cnt, status,
                                             static_cast<uint8_t*>(workspace) + kWsHeaderBytes, sms, st));
 }
 

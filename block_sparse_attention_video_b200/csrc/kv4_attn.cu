@@ -96,9 +96,11 @@ __device__ __forceinline__ uint32_t e4m3x2(uint32_t two_codes) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 // Bounded wait of a whole warp; one poll and a vote when the phase is there already.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, const Status& status) {
   if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity))) return true;
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
+  if (__all_sync(0xffffffffu, bounded_wait(bar, parity, abort_flag))) return true;
+  if ((threadIdx.x & 31) == 0) record_status(status, FVATTN_ERR_TIMEOUT);
+  return false;
 }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(float x) { return x; }
@@ -604,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : sizeof(T) == 4 ? 1 : 2
     if (!meet()) return;
     if (threadIdx.x == 0) {
       __threadfence();
-      sm.joiner = atomicAdd(P.arrived + begin, 1) == end - begin;
+      sm.joiner = arrive_at(P.arrived + begin, P.status.call) == end - begin;
       __threadfence();
     }
     if (!meet()) return;
@@ -663,8 +665,8 @@ cudaError_t launch_chunk(const AttnParams& P, int d, int grid, cudaStream_t st);
 // 411 and 314; one sequence of 32k, 12 heads: 17 rows 62 and 83, 40 rows 91 and 86.
 static bool many_rows(int max_q, int G) { return static_cast<long long>(max_q) * G > 32; }
 
-// Bytes behind the header that a call clears.
-size_t attn_ws_clear() { return align_up(kMaxBlocks * sizeof(int), 256); }
+// Bytes of the counters (cleared before a captured call).
+size_t attn_ws_clear() { return align_up(kMaxBlocks * sizeof(unsigned long long), 256); }
 size_t attn_ws_bytes(int d, int max_q, int G) {
   const size_t few = static_cast<size_t>(kMaxBlocks) * 2 * (16 * d + 32) * sizeof(float);
   const size_t part = many_rows(max_q, G) ? max(few, chunk_part_bytes(d, kMaxChunkBlocks)) : few;
@@ -683,7 +685,7 @@ static cudaError_t launch_stream(const AttnParams& P, int num_sms, cudaStream_t 
 
 cudaError_t launch_attn(const Cache& c, const Batch& bt, const void* q, long long q_stride, int Hq, void* out,
                         float* lse, bool bf16, float scale, int causal, int d, int block, int max_q, const int* kv_idx,
-                        const int* kv_cnt, int* status, uint8_t* ws, int num_sms, cudaStream_t st) {
+                        const int* kv_cnt, const Status& status, uint8_t* ws, int num_sms, cudaStream_t st) {
   AttnParams P;
   P.c = c;
   P.bt = bt;
@@ -698,7 +700,7 @@ cudaError_t launch_attn(const Cache& c, const Batch& bt, const void* q, long lon
   P.causal = causal;
   P.block = block;
   P.status = status;
-  P.arrived = reinterpret_cast<int*>(ws);
+  P.arrived = reinterpret_cast<unsigned long long*>(ws);
   P.part = reinterpret_cast<float*>(ws + attn_ws_clear());
   if (bf16 && !kv_idx && many_rows(max_q, P.G)) return launch_chunk(P, d, min(kMaxChunkBlocks, num_sms), st);
   // Up to eight query rows a unit, or sixteen.

@@ -120,7 +120,7 @@ __device__ void produce(const AttnParams& P, Smem<HD>& sm) {
   int b = 0, m0 = 0, seen = 0, which = 0, op = 0, un = 0, step = 0;
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, P.status));
+    return __all_sync(0xffffffffu, bounded_wait(bar, parity, abort_flag));
   };
   for (long long x = lo; ok;) {
     Meta m;
@@ -216,7 +216,7 @@ __device__ void expand(const AttnParams& P, Smem<HD>& sm) {
   const int shift = P.block == 128 ? 7 : 6;
   int op = 0, un = 0, step = 0;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, P.status));
+    return __all_sync(0xffffffffu, bounded_wait(bar, parity, abort_flag));
   };
   while (true) {
     const int u = un & 1;
@@ -291,7 +291,7 @@ __device__ void issue(const AttnParams& P, Smem<HD>& sm, uint32_t tmem) {
   const uint64_t dv = umma_desc_sw128(smem_u32(sm.kv[0]), T::kHalfBytes, 1024);
   int base = 0, un = 0, qn[2] = {0, 0}, pn[2] = {0, 0};
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, P.status));
+    return __all_sync(0xffffffffu, bounded_wait(bar, parity, abort_flag));
   };
   bool ok = true;
   while (ok) {
@@ -368,7 +368,7 @@ __device__ void softmax(const AttnParams& P, Smem<HD>& sm, uint32_t tmem) {
   const uint32_t tS = tmem + lane_off + X * 128, tO = tmem + lane_off + 256 + X * 128;
   int un = 0, sn = 0, on = 0, step = 0, met = 0;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, P.status));
+    return __all_sync(0xffffffffu, bounded_wait(bar, parity, abort_flag));
   };
 #pragma unroll 1
   while (true) {
@@ -571,7 +571,7 @@ __device__ void softmax(const AttnParams& P, Smem<HD>& sm, uint32_t tmem) {
     if (!meet()) return;
     if (row == 0) {   // one thread's fences, between the barriers, cover the slot's stores and loads
       __threadfence();
-      sm.joiner[X] = atomicAdd(P.arrived + begin * 2 + X, 1) == end - begin;
+      sm.joiner[X] = arrive_at(P.arrived + begin * 2 + X, P.status.call) == end - begin;
       __threadfence();
     }
     if (!meet()) return;
@@ -659,6 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const AttnParam
       __syncwarp();
       tc_fence_after();
       tmem_dealloc(tmem, 512);
+      if ((threadIdx.x & 31) == 0 && sm.abort_flag) record_status(P.status, FVATTN_ERR_TIMEOUT);
     }
   };
   if (warp >= 8) {

@@ -37,7 +37,7 @@ struct SelectParams {
   int k_min, block, stride;   // stride: scores per row in shared memory (max_pages, whole tiles of 8)
   int* kv_idx;
   int* kv_cnt;
-  int* status;
+  Status status;
 };
 
 __device__ __forceinline__ double warp_sum(double v) {
@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
   double* mass = G == 1 ? xs : xs + static_cast<size_t>(NP) * LD;    // [RU][LD]
   float* fmass = reinterpret_cast<float*>(xs + static_cast<size_t>(NP + (G == 1 ? 0 : RU)) * LD);   // [RU][LD]
   int* slots = reinterpret_cast<int*>(fmass + static_cast<size_t>(RU) * LD);                        // [LD]
+  open_call(P.status);
   seqs.load<kSelThreads>(P.bt);
   __syncthreads();
   const int *cu = seqs.rows_of(P.bt), *kv_len = seqs.lengths_of(P.bt);
@@ -440,7 +441,7 @@ static cudaError_t select_t(SelectParams& P, cudaStream_t st) {
 
 cudaError_t launch_select(const Cache& c, const Batch& bt, const void* q, long long q_stride, int Hq, bool bf16,
                           float scale, float p, int k_min, int d, int block, int* kv_idx, int* kv_cnt,
-                          int* status, cudaStream_t st) {
+                          const Status& status, cudaStream_t st) {
   SelectParams P;
   P.c = c;
   P.bt = bt;

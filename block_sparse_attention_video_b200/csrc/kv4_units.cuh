@@ -10,6 +10,7 @@
 #pragma once
 
 #include "kv4.cuh"
+#include "sm100.cuh"
 
 namespace fvattn {
 namespace kv4 {
@@ -19,6 +20,22 @@ constexpr float kFloor = -3.0e38f;                  // running max before any ke
 constexpr float kRaise = 8.f;                       // the max is raised when exceeded by 2^8
 constexpr float kHead = 6.f;                        // P <= 2^(6 + 8) stays inside fp16
 constexpr float kLn2 = 0.69314718055994531f;
+
+// mbar_wait of sm100.cuh without a status word: bounded, false on abort. A wait that runs out
+// raises the abort flag; who sees that at its end records FVATTN_ERR_TIMEOUT.
+__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  const uint32_t a = smem_u32(bar);
+  if (mbar_try_wait(a, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  while (true) {
+    if (mbar_try_wait(a, parity)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > kWaitTimeoutNs) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
 
 struct AttnParams {
   Cache c;
@@ -31,8 +48,8 @@ struct AttnParams {
   const int* kv_cnt;
   float scale_log2;       // scale * log2(e)
   int G, causal, block;
-  int* status;
-  int* arrived;           // [gridDim] blocks that left their part of the unit begun there
+  Status status;
+  unsigned long long* arrived;   // [gridDim] blocks that left their part of the unit begun there
   float* part;            // partial results of units that lie in several blocks
 };
 
@@ -156,6 +173,7 @@ struct Piece {
 // block that gets any.
 template <int RT, int kThreads>
 __device__ void find_piece(const AttnParams& P, Seqs& seqs, Piece& sm, int least) {
+  open_call(P.status);
   seqs.load<kThreads>(P.bt);
   __syncthreads();
   const Entries<RT> en(P, seqs);

@@ -167,10 +167,11 @@ __device__ __forceinline__ void add8(uint32_t codes, uint32_t scale, uint32_t (&
 template <typename T, int HD>
 __global__ void __launch_bounds__(kWriteThreads, sizeof(T) == 2 ? 4 : 3)
     append_kernel(const Cache c, const Batch bt, const T* __restrict__ k, const T* __restrict__ v,
-                  long long k_stride, long long v_stride, int block, int* status) {
+                  long long k_stride, long long v_stride, int block, const Status status) {
   constexpr int LPR = HD / 8;                 // lanes per row
   constexpr int RPB = kWriteThreads / LPR;    // rows per pass of the block
   __shared__ Seqs seqs;
+  open_call(status);
   seqs.load<kWriteThreads>(bt);
   __syncthreads();
   const int *cu = seqs.rows_of(bt), *kv_len = seqs.lengths_of(bt);
@@ -276,10 +277,11 @@ __device__ __forceinline__ void decode8(uint32_t codes, uint32_t scale, float he
 // lie is looked up once, a thread a row.
 template <typename T, int HD>
 __global__ void __launch_bounds__(kWriteThreads)
-    read_kernel(const Cache c, const Batch bt, T* __restrict__ k_out, T* __restrict__ v_out, int block, int* status) {
+    read_kernel(const Cache c, const Batch bt, T* __restrict__ k_out, T* __restrict__ v_out, int block, const Status status) {
   constexpr int LPR = HD / 8, GROUPS = kWriteThreads / LPR, EACH = 8, UNITS = GROUPS * EACH;
   __shared__ int2 place[UNITS + 1];                   // pool slot (-1: invalid, -2: no row) and position in the page
   __shared__ Seqs seqs;
+  open_call(status);
   seqs.load<kWriteThreads>(bt);
   __syncthreads();
   const int *cu = seqs.rows_of(bt), *kv_len = seqs.lengths_of(bt);
@@ -346,7 +348,7 @@ __global__ void __launch_bounds__(kWriteThreads)
 
 template <typename T>
 static cudaError_t append_t(const Cache& c, const Batch& bt, const void* k, const void* v, long long ks,
-                            long long vs, int d, int block, int* status, cudaStream_t st) {
+                            long long vs, int d, int block, const Status& status, cudaStream_t st) {
   const long long grid = (static_cast<long long>(bt.rows) / block + 2ll * bt.B) * c.H;
   if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;
   const T* kt = static_cast<const T*>(k);
@@ -359,7 +361,7 @@ static cudaError_t append_t(const Cache& c, const Batch& bt, const void* k, cons
 }
 
 template <typename T>
-static cudaError_t read_t(const Cache& c, const Batch& bt, void* k, void* v, int d, int block, int* status,
+static cudaError_t read_t(const Cache& c, const Batch& bt, void* k, void* v, int d, int block, const Status& status,
                           cudaStream_t st) {
   const long long per = kWriteThreads / (d / 8) * 8;
   const long long grid = (static_cast<long long>(bt.rows) * c.H + per - 1) / per;
@@ -374,13 +376,13 @@ static cudaError_t read_t(const Cache& c, const Batch& bt, void* k, void* v, int
 }
 
 cudaError_t launch_append(const Cache& c, const Batch& bt, const void* k, const void* v, long long ks,
-                          long long vs, bool bf16, int d, int block, int* status, cudaStream_t st) {
+                          long long vs, bool bf16, int d, int block, const Status& status, cudaStream_t st) {
   return bf16 ? append_t<__nv_bfloat16>(c, bt, k, v, ks, vs, d, block, status, st)
               : append_t<float>(c, bt, k, v, ks, vs, d, block, status, st);
 }
 
 cudaError_t launch_read(const Cache& c, const Batch& bt, void* k, void* v, bool bf16, int d, int block,
-                        int* status, cudaStream_t st) {
+                        const Status& status, cudaStream_t st) {
   return bf16 ? read_t<__nv_bfloat16>(c, bt, k, v, d, block, status, st)
               : read_t<float>(c, bt, k, v, d, block, status, st);
 }
