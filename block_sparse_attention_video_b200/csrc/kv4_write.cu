@@ -272,13 +272,14 @@ __device__ __forceinline__ void decode8(uint32_t codes, uint32_t scale, float he
   store8(out, x);
 }
 
-// A block reads 8 (row, KV head) pairs for every group of HD/8 lanes, neighbouring groups on
+// A block reads EACH (row, KV head) pairs for every group of HD/8 lanes, neighbouring groups on
 // neighbouring heads so that the outputs are written in one stream. Where the block's rows
 // lie is looked up once, a thread a row.
-template <typename T, int HD>
+template <typename T, int HD, int EACH>
 __global__ void __launch_bounds__(kWriteThreads)
     read_kernel(const Cache c, const Batch bt, T* __restrict__ k_out, T* __restrict__ v_out, int block, const Status status) {
-  constexpr int LPR = HD / 8, GROUPS = kWriteThreads / LPR, EACH = 8, UNITS = GROUPS * EACH;
+  constexpr int LPR = HD / 8, GROUPS = kWriteThreads / LPR, UNITS = GROUPS * EACH;
+  constexpr int BATCH = EACH < 4 ? EACH : 4;          // pairs whose loads are in flight together
   __shared__ int2 place[UNITS + 1];                   // pool slot (-1: invalid, -2: no row) and position in the page
   __shared__ Seqs seqs;
   open_call(status);
@@ -312,12 +313,12 @@ __global__ void __launch_bounds__(kWriteThreads)
   const Layout L(HD, block);
   const int l = threadIdx.x % LPR, g = threadIdx.x / LPR;
 #pragma unroll
-  for (int part = 0; part < EACH; part += 4) {
-    uint32_t w[4][2], sc[4][2];
-    int slot[4];
-    unsigned head[4];
+  for (int part = 0; part < EACH; part += BATCH) {
+    uint32_t w[BATCH][2], sc[BATCH][2];
+    int slot[BATCH];
+    unsigned head[BATCH];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < BATCH; ++i) {
       const unsigned u = u0 + (part + i) * GROUPS + g, r = u / H;
       slot[i] = -2;
       head[i] = u - r * H;
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(kWriteThreads)
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < BATCH; ++i) {
       if (slot[i] == -2) continue;
       const size_t at = static_cast<size_t>(u0 + (part + i) * GROUPS + g) * HD + l * 8;
       decode8(w[i][0], sc[i][0], c.k_scale ? __ldg(c.k_scale + head[i]) : 1.f, k_out + at);
@@ -360,19 +361,32 @@ static cudaError_t append_t(const Cache& c, const Batch& bt, const void* k, cons
   return cudaGetLastError();
 }
 
+template <typename T, int HD, int EACH>
+static cudaError_t read_launch(const Cache& c, const Batch& bt, void* k, void* v, int block, const Status& status,
+                               cudaStream_t st) {
+  const long long per = kWriteThreads / (HD / 8) * EACH;
+  const long long grid = (static_cast<long long>(bt.rows) * c.H + per - 1) / per;
+  if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  read_kernel<T, HD, EACH><<<static_cast<unsigned>(grid), kWriteThreads, 0, st>>>(c, bt, static_cast<T*>(k),
+                                                                                static_cast<T*>(v), block, status);
+  return cudaGetLastError();
+}
+
+template <typename T, int HD>
+static cudaError_t read_hd(const Cache& c, const Batch& bt, void* k, void* v, int block, const Status& status,
+                           cudaStream_t st) {
+  // Eight pairs a lane group share the block's look-ups (393,120 pairs at d 128: 53 us, 68 with
+  // one); one where eight would leave SMs without a block (3,700 pairs at d 64: 4.2 us, 8.6 with
+  // eight).
+  if (static_cast<long long>(bt.rows) * c.H < 148ll * 8 * (kWriteThreads / (HD / 8)))
+    return read_launch<T, HD, 1>(c, bt, k, v, block, status, st);
+  return read_launch<T, HD, 8>(c, bt, k, v, block, status, st);
+}
+
 template <typename T>
 static cudaError_t read_t(const Cache& c, const Batch& bt, void* k, void* v, int d, int block, const Status& status,
                           cudaStream_t st) {
-  const long long per = kWriteThreads / (d / 8) * 8;
-  const long long grid = (static_cast<long long>(bt.rows) * c.H + per - 1) / per;
-  if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  T* kt = static_cast<T*>(k);
-  T* vt = static_cast<T*>(v);
-  if (d == 128)
-    read_kernel<T, 128><<<static_cast<unsigned>(grid), kWriteThreads, 0, st>>>(c, bt, kt, vt, block, status);
-  else
-    read_kernel<T, 64><<<static_cast<unsigned>(grid), kWriteThreads, 0, st>>>(c, bt, kt, vt, block, status);
-  return cudaGetLastError();
+  return d == 128 ? read_hd<T, 128>(c, bt, k, v, block, status, st) : read_hd<T, 64>(c, bt, k, v, block, status, st);
 }
 
 cudaError_t launch_append(const Cache& c, const Batch& bt, const void* k, const void* v, long long ks,
