@@ -59,18 +59,6 @@ __device__ __forceinline__ void record_status(const Status& s, int code) {
   }
 }
 
-// Arrival at a counter that need not be cleared either: call << 16 | arrivals. Returns how many
-// of this call came before.
-__device__ __forceinline__ int arrive_at(unsigned long long* word, unsigned long long call) {
-  unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(word);
-  while (true) {
-    const unsigned long long base = (old >> 16) == call ? old : call << 16;
-    const unsigned long long seen = atomicCAS(word, old, base + 1);
-    if (seen == old) return static_cast<int>(base & 0xFFFFu);
-    old = seen;
-  }
-}
-
 // A sequence's length n, clamped to what its table row can hold.
 __device__ __forceinline__ int held(int n, const Batch& bt, int block, const Status& status) {
   const int most = bt.max_pages * block;

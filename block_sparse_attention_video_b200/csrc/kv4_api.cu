@@ -100,7 +100,7 @@ fvattn_status begin(void* ws, size_t have, size_t need, cudaStream_t st, int row
   const bool known = cudaStreamIsCapturing(st, &cap) == cudaSuccess;
   if (!known) cudaGetLastError();
   if (known && cap == cudaStreamCaptureStatusNone && rows > 0) return FVATTN_OK;
-  clear_kernel<<<1, 128, 0, st>>>(static_cast<uint4*>(ws), static_cast<int>((kWsHeaderBytes + clear) / 16));
+  clear_kernel<<<1, 512, 0, st>>>(static_cast<uint4*>(ws), static_cast<int>((kWsHeaderBytes + clear) / 16));
   return cudaGetLastError() == cudaSuccess ? FVATTN_OK : FVATTN_ERR_CUDA;
 }
 

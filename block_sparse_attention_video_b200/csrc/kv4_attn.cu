@@ -601,13 +601,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : sizeof(T) == 4 ? 1 : 2
       }
     }
     if (whole) continue;
-    // ---- the unit lies in blocks begin .. end: the last to arrive joins them in order
-    // (one thread's fences, between the barriers, cover the whole block's stores and loads)
+    // ---- the unit lies in blocks begin .. end: who finds all parts there joins them in order
+    // (one warp's fences, between the barriers, cover the whole block's stores and loads)
     if (!meet()) return;
-    if (threadIdx.x == 0) {
-      __threadfence();
-      sm.joiner = arrive_at(P.arrived + begin, P.status.call) == end - begin;
-      __threadfence();
+    if (warp == 0) {
+      const bool all = leave_part(P.left, P.status.call, begin, end, [&](int i) { return 2 * i + (i == begin ? 1 : 0); });
+      if (lane == 0) sm.joiner = all;
     }
     if (!meet()) return;
     if (!sm.joiner) continue;
@@ -653,9 +652,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : sizeof(T) == 4 ? 1 : 2
   }
 }
 
-// Workspace behind the header: arrival counters, then partial results.
+// Workspace behind the header: flags of the parts left, then the partial results.
 constexpr int kMaxBlocks = 448;                    // three blocks on each of 148 SMs
 constexpr int kMaxChunkBlocks = 160;
+static_assert(kMaxChunkBlocks * 4 <= kMaxBlocks * 2, "");
 
 size_t chunk_part_bytes(int d, int grid);
 cudaError_t launch_chunk(const AttnParams& P, int d, int grid, cudaStream_t st);
@@ -665,8 +665,8 @@ cudaError_t launch_chunk(const AttnParams& P, int d, int grid, cudaStream_t st);
 // 411 and 314; one sequence of 32k, 12 heads: 17 rows 62 and 83, 40 rows 91 and 86.
 static bool many_rows(int max_q, int G) { return static_cast<long long>(max_q) * G > 32; }
 
-// Bytes of the counters (cleared before a captured call).
-size_t attn_ws_clear() { return align_up(kMaxBlocks * sizeof(unsigned long long), 256); }
+// Bytes of the flags, two a block (here) or four (kMaxChunkBlocks); cleared before a captured call.
+size_t attn_ws_clear() { return align_up(kMaxBlocks * 2 * sizeof(unsigned long long), 256); }
 size_t attn_ws_bytes(int d, int max_q, int G) {
   const size_t few = static_cast<size_t>(kMaxBlocks) * 2 * (16 * d + 32) * sizeof(float);
   const size_t part = many_rows(max_q, G) ? max(few, chunk_part_bytes(d, kMaxChunkBlocks)) : few;
@@ -700,7 +700,7 @@ cudaError_t launch_attn(const Cache& c, const Batch& bt, const void* q, long lon
   P.causal = causal;
   P.block = block;
   P.status = status;
-  P.arrived = reinterpret_cast<unsigned long long*>(ws);
+  P.left = reinterpret_cast<unsigned long long*>(ws);
   P.part = reinterpret_cast<float*>(ws + attn_ws_clear());
   if (bf16 && !kv_idx && many_rows(max_q, P.G)) return launch_chunk(P, d, min(kMaxChunkBlocks, num_sms), st);
   // Up to eight query rows a unit, or sixteen.

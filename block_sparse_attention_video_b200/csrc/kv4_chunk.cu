@@ -543,7 +543,7 @@ __device__ void softmax(const AttnParams& P, Smem<HD>& sm, uint32_t tmem) {
       continue;
     }
     // The unit lies in blocks begin .. end: O to the workspace ([HD/4][128] float4, a row a
-    // thread), and the last slot to arrive joins them in the order of the blocks.
+    // thread), and who finds all parts there joins them in the order of the blocks.
     auto part_of = [&](int i) {
       return P.part + ((static_cast<size_t>(i) * 2 + (i == begin ? 1 : 0)) * 2 + X) * T::kPart;
     };
@@ -569,10 +569,10 @@ __device__ void softmax(const AttnParams& P, Smem<HD>& sm, uint32_t tmem) {
       return wait(&sm.meet[X], met++ & 1);
     };
     if (!meet()) return;
-    if (row == 0) {   // one thread's fences, between the barriers, cover the slot's stores and loads
-      __threadfence();
-      sm.joiner[X] = arrive_at(P.arrived + begin * 2 + X, P.status.call) == end - begin;
-      __threadfence();
+    if (quad == 0) {   // one warp's fences, between the barriers, cover the slot's stores and loads
+      const bool all = leave_part(P.left, P.status.call, begin, end,
+                                  [&](int i) { return (2 * i + (i == begin ? 1 : 0)) * 2 + X; });
+      if (lane == 0) sm.joiner[X] = all;
     }
     if (!meet()) return;
     if (!sm.joiner[X]) continue;

@@ -5,8 +5,8 @@
 // 128 keys: one page of 128 tokens or two of 64. The steps of all units form one line that is
 // cut into equal pieces, one per block, so ragged and causal lengths balance by themselves:
 // every block adds up the units' lengths and finds its piece. A unit that lies in several
-// pieces leaves partial sums in the workspace; the block that arrives last joins them in the
-// order of the pieces, so the result does not depend on who that is.
+// pieces leaves partial sums in the workspace; the block that finds them all there joins them in
+// the order of the pieces, so the result does not depend on who that is.
 #pragma once
 
 #include "kv4.cuh"
@@ -49,7 +49,7 @@ struct AttnParams {
   float scale_log2;       // scale * log2(e)
   int G, causal, block;
   Status status;
-  unsigned long long* arrived;   // [gridDim] blocks that left their part of the unit begun there
+  unsigned long long* left;      // flags of the parts left in `part`: the number of the call that left them
   float* part;            // partial results of units that lie in several blocks
 };
 
@@ -222,6 +222,31 @@ __device__ void find_piece(const AttnParams& P, Seqs& seqs, Piece& sm, int least
     }
   }
   __syncthreads();
+}
+
+// Marks a block's part of a unit as left, and tells whether all parts of the unit are: flags[at(i)]
+// for i in begin .. end, each the number of the call that left the part. Whole warp, after a barrier
+// that orders the block's stores of the part. Every block stores its flag before it looks at the
+// others' (sequentially consistent fences between), so the last one to store sees them all; should
+// another see them too, both join the same parts to the same result. No counter is incremented:
+// nothing has to be reset, and blocks do not queue for one word.
+template <typename At>
+__device__ __forceinline__ bool leave_part(unsigned long long* flags, unsigned long long call, int begin, int end,
+                                           At&& at) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) {
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(flags + at(static_cast<int>(blockIdx.x))), "l"(call)
+                 : "memory");
+    asm volatile("fence.sc.gpu;" ::: "memory");
+  }
+  __syncwarp();
+  bool all = true;
+  for (int i = begin + lane; i <= end; i += 32) {
+    unsigned long long f;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(f) : "l"(flags + at(i)) : "memory");
+    all = all && f == call;
+  }
+  return __all_sync(0xffffffffu, all);
 }
 
 // Block that holds position x of the line: the largest i with floor(total i / blocks) <= x,
