@@ -257,17 +257,21 @@ __global__ void __launch_bounds__(kWriteThreads, sizeof(T) == 2 ? 4 : 3)
   }
 }
 
+// Eight codes to T. A code times its scale is exact in fp16; the head's scale, where there is one,
+// is the one fp32 rounding.
 template <typename T>
-__device__ __forceinline__ void decode8(uint32_t codes, uint32_t scale, float head_scale, T* out) {
-  const float s = e4m3_to_float(scale);
+__device__ __forceinline__ void decode8(uint32_t codes, uint32_t scale, const float* head_scales, int h, T* out) {
+  const __half2 two = e4m3x2_to_half2(scale | scale << 8);
+  const float hs = head_scales ? __ldg(head_scales + h) : 1.f;
   uint32_t p[4];
   e2m1x8_to_half2(codes, p);
   float x[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
-    x[2 * i] = f.x * s * head_scale;                  // f * s is exact: one rounding
-    x[2 * i + 1] = f.y * s * head_scale;
+    float2 f = __half22float2(__hmul2(*reinterpret_cast<const __half2*>(&p[i]), two));
+    if (head_scales) f = __fmul2_rn(f, make_float2(hs, hs));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
   }
   store8(out, x);
 }
@@ -341,8 +345,8 @@ __global__ void __launch_bounds__(kWriteThreads)
     for (int i = 0; i < BATCH; ++i) {
       if (slot[i] == -2) continue;
       const size_t at = static_cast<size_t>(u0 + (part + i) * GROUPS + g) * HD + l * 8;
-      decode8(w[i][0], sc[i][0], c.k_scale ? __ldg(c.k_scale + head[i]) : 1.f, k_out + at);
-      decode8(w[i][1], sc[i][1], c.v_scale ? __ldg(c.v_scale + head[i]) : 1.f, v_out + at);
+      decode8(w[i][0], sc[i][0], c.k_scale, head[i], k_out + at);
+      decode8(w[i][1], sc[i][1], c.v_scale, head[i], v_out + at);
     }
   }
 }
