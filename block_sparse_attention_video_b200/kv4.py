@@ -256,6 +256,12 @@ class KV4Path:
         if rows > self.max_rows or batch.B > self.max_batch or batch.max_pages != self.max_pages:
             raise ValueError(f"{rows} rows of {batch.B} sequences with {batch.max_pages} pages do not fit the path "
                              f"({self.max_rows}, {self.max_batch}, {self.max_pages})")
+        # all of it before the first call writes into the cache
+        if q.shape[1:] != self.out.shape[1:] or q.dtype != self.out.dtype:
+            raise ValueError(f"q is {tuple(q.shape)} {q.dtype}, the path's rows are {tuple(self.out.shape[1:])} "
+                             f"{self.out.dtype}")
+        if k.shape[0] != rows or v.shape[0] != rows:
+            raise ValueError(f"q has {rows} rows, k {k.shape[0]} and v {v.shape[0]}")
         fvattn_kv4_append(self.cache, batch, k, v, self.ws_append)
         idx = cnt = None
         if self.p is not None:

@@ -808,16 +808,97 @@ def test_two_calls_at_once_and_repeats_are_bit_identical():
 
 
 def test_an_explicit_stream_is_used():
+    """The call stands behind the work of the stream it names, not of the current one."""
     c = Case([500], [1], 1, 64, 64, seed=25, Hq=4)
     q = c.make_q().cuda()
-    want, _ = c.attend(q)
-    torch.cuda.synchronize()
+    want, want_lse = c.attend(q)
+    late, out, lse, ws = torch.zeros_like(q), torch.zeros_like(q), torch.zeros_like(want_lse), c.ws(F.FVATTN_OP_KV4_ATTN, 1)
     s = torch.cuda.Stream()
-    got, _ = c.attend(q, stream=s)
-    s.synchronize()
-    # the buffers were filled on the current stream before: wait for both
     torch.cuda.synchronize()
-    assert got.shape == want.shape
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)                       # some 10 ms
+        late.copy_(q)
+    F.fvattn_kv4_attn(c.cache, c.batch, late, out, ws, lse=lse, stream=s)
+    s.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("fill", [0x00, 0xFF, 0x5E])
+def test_what_a_workspace_holds_does_not_matter(rows, fill):
+    """Eager calls clear nothing: any bytes may lie there, the parts of other calls too."""
+    c = Case([9000, 77], [rows, 1], 2, 128, 128, seed=50, Hq=4)
+    q = c.make_q().cuda()
+    out, lse = c.attend(q)
+    c.check(q.cpu(), out, lse, rows=[0, rows])
+    c.last_ws.view(torch.uint8).fill_(fill)
+    other = c.make_q(spread=3.0).cuda()
+    c.attend(other, ws=c.last_ws)                           # leaves parts of the same units
+    again = c.attend(q, ws=c.last_ws)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    assert F.fvattn_workspace_status(c.last_ws) == F.FVATTN_OK
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_replays_and_eager_calls_share_a_workspace(rows):
+    """Replays of a captured call share its number; units that several blocks hold are joined right in each,
+    with eager calls between, and an error is the last call's only."""
+    c = Case([9000, 77], [rows, 1], 2, 128, 128, seed=51, Hq=4)
+    q = c.make_q().cuda()
+    ws = c.ws(F.FVATTN_OP_KV4_ATTN, rows + 1)
+    batch = c.batch_of(c.nrow)
+    kv = batch.kv_len.clone()
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    run = lambda: F.fvattn_kv4_attn(c.cache, batch, q, out, ws, lse=lse)
+    run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for step in range(8):
+        q.copy_(c.make_q(spread=1.0 + step))
+        bad = step in (2, 3, 6)
+        batch.kv_len.copy_(kv)
+        if bad:
+            batch.kv_len[1] = c.max_pages * c.block + 1     # clamped, and its last page is in no table
+        out.fill_(77.0)
+        run() if step % 3 == 1 else graph.replay()
+        assert F.fvattn_workspace_status(ws) == (F.FVATTN_ERR_INVALID_ARG if bad else F.FVATTN_OK), step
+        if not bad:
+            want = c.attend(q)
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1]), step
+            c.check(q.cpu(), out, lse, rows=[0, rows])
+
+
+def test_status_of_a_workspace_that_other_calls_use_too():
+    """The status is the last call's, whichever kind of call it was."""
+    c = Case([300], [2], 1, 64, 64, seed=52, Hq=2)
+    q = c.make_q().cuda()
+    ws = F.alloc_workspace(1 << 22, "cuda")
+    bad = F.KV4Batch(c.table, torch.tensor([-1], dtype=torch.int32, device="cuda"), c.batch.cu, 2)
+    out = torch.empty_like(q)
+    dense = [torch.randn((1, 1, 128, 64), device="cuda").to(BF16) for _ in range(3)]
+    for batch, want in ((bad, F.FVATTN_ERR_INVALID_ARG), (c.batch, F.FVATTN_OK)):
+        F.fvattn_kv4_attn(c.cache, batch, q, out, ws)
+        assert F.fvattn_workspace_status(ws) == want
+        F.fvattn_dense_fwd(*dense, torch.empty_like(dense[0]), 128, 64, ws)
+        assert F.fvattn_workspace_status(ws) == F.FVATTN_OK
+        F.fvattn_kv4_attn(c.cache, batch, q, out, ws)
+        assert F.fvattn_workspace_status(ws) == want
+    e = torch.empty((0, 2, 64), dtype=BF16, device="cuda")
+    F.fvattn_kv4_attn(c.cache, bad, e, e.clone(), ws)       # a call without rows looks at nothing
+    assert F.fvattn_workspace_status(ws) == F.FVATTN_OK
+
+
+def test_the_path_refuses_before_it_writes():
+    c = Case([100, 60], [1, 1], 2, 64, 64, seed=53, Hq=4)
+    path = F.KV4Path(c.cache, 4, 2, 2, c.max_pages, BF16, p=0.5)
+    q, k, v = (t.cuda() for t in _path_inputs(c, 2, 3))
+    before = c.cache.pages.clone()
+    for bad in ((q[:1], k, v), (q, k[:1], v[:1]), (q, k, v[:1]), (q.float(), k, v), (q[:, :2], k, v),
+                (q.repeat(2, 1, 1), k.repeat(2, 1, 1), v.repeat(2, 1, 1))):
+        with pytest.raises((ValueError, TypeError)):
+            path(c.batch, *bad)
+    assert torch.equal(before, c.cache.pages)
 
 
 def test_no_rows():
