@@ -2,6 +2,7 @@
 // (declared in include/fvattn.h): host-side validation, workspace layout, dispatch.
 // No entry point allocates device memory or synchronizes the host.
 #include <atomic>
+#include <chrono>
 #include <cmath>
 
 #include "kv4.cuh"
@@ -86,6 +87,15 @@ __global__ void clear_kernel(uint4* p, int n) {
   for (int i = threadIdx.x; i < n; i += blockDim.x) p[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
+// Where the calls' numbers start: somewhere else in every process and every copy of the library, so
+// that memory which another one's calls have left flags in does not carry the numbers of this one's.
+unsigned long long first_number() {
+  unsigned long long x = static_cast<unsigned long long>(std::chrono::system_clock::now().time_since_epoch().count());
+  x ^= static_cast<unsigned long long>(reinterpret_cast<uintptr_t>(&first_number)) << 20;
+  x *= 0x9E3779B97F4A7C15ull;                 // 2^64 / golden ratio: all bits reach the upper ones
+  return 1ull + (x >> 17);                    // 1 .. 2^47
+}
+
 // Workspace check, and the call's number (kv4.cuh). The header and `clear` bytes of counters behind
 // it are cleared only where that does not do: in a captured call, whose replays share the number,
 // and in a call without rows, which runs no other kernel. A clearing launch costs 2 us of host time
@@ -93,7 +103,7 @@ __global__ void clear_kernel(uint4* p, int n) {
 fvattn_status begin(void* ws, size_t have, size_t need, cudaStream_t st, int rows, fvattn::kv4::Status* status,
                     size_t clear = 0) {
   if (!ws || !aligned(ws, 256) || have < need) return FVATTN_ERR_WORKSPACE;
-  static std::atomic<unsigned long long> calls{0x5EED00000001ull};
+  static std::atomic<unsigned long long> calls{first_number()};
   status->h = static_cast<fvattn::WsHeader*>(ws);
   status->call = calls.fetch_add(1, std::memory_order_relaxed) & 0xFFFFFFFFFFFFull;
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
