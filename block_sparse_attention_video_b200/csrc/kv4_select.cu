@@ -6,10 +6,12 @@
 // differs from its definition by a few 2^-53 and only true ties are decided by rounding.
 //
 // One block per group of rows of a sequence and KV head. Up to eight (row, query head)
-// pairs share every page's sum, which is converted to fp64 once for all of them; what
-// bounds a call of many rows is the fp64 units (d multiply-adds a pair and page, 64 a
-// clock and SM), of single tokens HBM (4 d bytes a page).
-//   1. scores: fp64 tensor products of 8 pairs x 8 pages x 4 channels. q stays in registers;
+// pairs share every page's sum, which is converted to fp64 once for all of them. The floor of
+// a call of many rows is the fp64 units (d multiply-adds a pair and page, 64 a clock and
+// SM), of single tokens HBM (4 d bytes a page); what bounds both is the latency of one
+// block's chain (look-up, scores, softmax, search: a third of it each of the last three), so
+// loads go out several at a time and, in large grids, three blocks share an SM.
+//   1. scores: fp64 tensor products of 8 pairs x 8 pages x 4 channels. q lies in shared memory;
 //      a page's sums are loaded straight into the operand's lanes (the order of channels in
 //      a dot product is free: lane t of a quad takes channels 16 i + 4 t .. + 3, 16 bytes).
 //   2. softmax of each pair over its pages and the mean over a row's pairs, in shared memory.
@@ -23,6 +25,7 @@ namespace fvattn {
 namespace kv4 {
 
 constexpr int kSelThreads = 256;
+constexpr int kAtOnce = 4;     // masses a lane loads before it looks at the first
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_float(float x) { return x; }
 
@@ -121,34 +124,51 @@ __device__ bool quick_cut(const double* x, const float* f, int n, float p, doubl
   int c_lo = n, c_hi = 0;                    // c_lo: an upper bound until a probe has moved lo
   while (c_lo - c_hi > 32) {
     if (hi <= lo + 1u) return false;
-    const unsigned mid = lo + ((hi - lo) >> 1);
-    const float v = __uint_as_float(mid);
-    float a = 0.f;
-    int c = 0;
+    // three probes a pass, at the quarters: a pass waits for its loads and reductions
+    const unsigned quarter = (hi - lo) >> 2, mid[3] = {lo + quarter, lo + ((hi - lo) >> 1), hi - max(quarter, 1u)};
+    float a[3] = {0.f, 0.f, 0.f};
+    int c[3] = {0, 0, 0};
 #pragma unroll 4
     for (int j = lane; j < n; j += 32) {
       const float m = f[j];
-      const bool ge = m >= v;
-      a += ge ? m : 0.f;
-      c += ge ? 1 : 0;
+#pragma unroll
+      for (int u = 0; u < 3; ++u) {
+        const bool ge = m >= __uint_as_float(mid[u]);
+        a[u] += ge ? m : 0.f;
+        c[u] += ge ? 1 : 0;
+      }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-    c = __reduce_add_sync(0xffffffffu, c);
-    if (a >= p + kClear) { lo = mid; c_lo = c; }
-    else if (a < p - kClear) { hi = mid; c_hi = c; }
-    else return false;
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int u = 0; u < 3; ++u) a[u] += __shfl_xor_sync(0xffffffffu, a[u], o);
+    const unsigned lo0 = lo, hi0 = hi;
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+      c[u] = __reduce_add_sync(0xffffffffu, c[u]);
+      if (a[u] >= p + kClear) { lo = mid[u]; c_lo = c[u]; }
+      else if (a[u] < p - kClear && hi == hi0) { hi = mid[u]; c_hi = c[u]; }
+    }
+    if (lo == lo0 && hi == hi0) return false;
   }
   const float vlo = __uint_as_float(lo), vhi = __uint_as_float(hi);
   double above = 0.0;
   int have = 0;
-#pragma unroll 2
-  for (int j0 = 0; j0 < n; j0 += 32) {
-    const int j = j0 + lane;
-    const float m = j < n ? f[j] : -1.f;
-    const double d = j < n ? x[j] : 0.0;
-    if (m >= vhi) above += d;
-    gather32(d, m >= vlo && m < vhi, box, have);
+#pragma unroll 1
+  for (int j0 = 0; j0 < n; j0 += 32 * kAtOnce) {
+    float m[kAtOnce];
+    double d[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int j = j0 + 32 * u + lane;
+      m[u] = j < n ? f[j] : -1.f;
+      d[u] = j < n ? x[j] : 0.0;
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      above += m[u] >= vhi ? d[u] : 0.0;
+      gather32(d[u], m[u] >= vlo && m[u] < vhi, box, have);
+    }
   }
   above = warp_sum(above);
   const double target = static_cast<double>(p);
@@ -239,16 +259,28 @@ __device__ void pick_pages(const double* x, const float* f, int n, float p, int 
   // all pages above v*, and at v* the first ones that fill the count
   const int take = all ? 0 : cut.cnt - cut.above;
   int written = 0, tied = 0;
-  for (int j0 = 0; j0 < n; j0 += 32) {
-    const int j = j0 + lane;
-    const double m = j < n ? x[j] : -1.0;
-    const bool eq = !all && m == cut.star;
-    const unsigned eqs = __ballot_sync(0xffffffffu, eq);
-    const bool sel = j < n && (all || m > cut.star || (eq && tied + __popc(eqs & below) < take));
-    const unsigned sels = __ballot_sync(0xffffffffu, sel);
-    if (sel) out[written + __popc(sels & below)] = j;
-    written += __popc(sels);
-    tied += __popc(eqs);
+  // (masses are not negative, so their bit patterns compare as they do; 64-bit float compares wait
+  // for the fp64 units. Where a mass is a NaN, all pages are taken.)
+  const long long star = all ? 0 : __double_as_longlong(cut.star);
+#pragma unroll 1
+  for (int j0 = 0; j0 < n; j0 += 32 * kAtOnce) {
+    long long m[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int j = j0 + 32 * u + lane;
+      m[u] = j < n ? __double_as_longlong(x[j]) : -1ll;
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int j = j0 + 32 * u + lane;
+      const bool eq = !all && m[u] == star;
+      const unsigned eqs = __ballot_sync(0xffffffffu, eq);
+      const bool sel = j < n && (all || m[u] > star || (eq && tied + __popc(eqs & below) < take));
+      const unsigned sels = __ballot_sync(0xffffffffu, sel);
+      if (sel) out[written + __popc(sels & below)] = j;
+      written += __popc(sels);
+      tied += __popc(eqs);
+    }
   }
   if (lane == 0) {
     out[written] = n;
@@ -264,9 +296,11 @@ __device__ __forceinline__ void mma_f64(double (&c)[2], double a, double b) {
       : "d"(a), "d"(b));
 }
 
-template <typename T, int HD>
-__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectParams P) {
+// Three blocks share an SM (kThree) or two, which then have the registers to fetch ahead.
+template <typename T, int HD, bool kThree>
+__global__ void __launch_bounds__(kSelThreads, kThree ? 3 : 2) select_kernel(const SelectParams P) {
   constexpr int PAIRS = 8, kWarps = kSelThreads / 32;
+  static_assert(PAIRS == kWarps, "a warp brings a pair's q");
   extern __shared__ __align__(16) uint8_t raw[];
   __shared__ __align__(16) double qs[PAIRS][HD + 2];   // two off: the quads' reads take all banks
   __shared__ double scale[PAIRS];                      // 1 / (sum of a pair's exponentials * G)
@@ -300,7 +334,6 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
   const int most = pos0 + rows - 1 < 0 ? 0 : (pos0 + rows - 1) / P.block;   // pages to score
   const double w = P.w * (P.c.k_scale ? static_cast<double>(__ldg(P.c.k_scale + h)) : 1.0);
   const int chunks = (G + NP - 1) / NP;                              // of query heads; one if RU > 1
-  for (int j = tid; j < most; j += kSelThreads) slots[j] = pool_slot(P.bt, P.c.num_pages, b, j, P.status);
   // Pages that row i of the group scores; 0 for a row before the sequence (recorded below).
   auto own_of = [&](int i) { return i < rows && pos0 + i >= 0 ? (pos0 + i) / P.block : 0; };
   for (int ch = 0; ch < chunks; ++ch) {
@@ -308,16 +341,21 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
     auto row_of = [&](int k) { return RU > 1 ? k / G : 0; };
     auto head_of = [&](int k) { return RU > 1 ? k % G : ch * NP + k; };
     auto live = [&](int k) { return k < NP && row_of(k) < rows && (RU > 1 ? k < RU * G : head_of(k) < G); };
-    for (int i = tid; i < PAIRS * HD; i += kSelThreads) {
-      const int k = i / HD, c = i % HD;
-      qs[k][c] = !live(k) ? 0.0
-                          : static_cast<double>(to_float(
-                                static_cast<const T*>(P.q)[static_cast<long long>(first + row_of(k)) * P.q_stride +
-                                                           (static_cast<long long>(h) * G + head_of(k)) * HD + c]));
-    }
+    // a warp brings a pair's q; the pool slots are looked up while it is on its way
+    struct alignas(sizeof(T) * HD / 32) Part { T x[HD / 32]; } part;
+    const bool here = live(warp);
+    if (here)
+      part = *reinterpret_cast<const Part*>(static_cast<const T*>(P.q) +
+                                            static_cast<long long>(first + row_of(warp)) * P.q_stride +
+                                            (static_cast<long long>(h) * G + head_of(warp)) * HD + lane * (HD / 32));
+    if (ch == 0)
+      for (int j = tid; j < most; j += kSelThreads) slots[j] = pool_slot(P.bt, P.c.num_pages, b, j, P.status);
+#pragma unroll
+    for (int i = 0; i < HD / 32; ++i)
+      qs[warp][lane * (HD / 32) + i] = here ? static_cast<double>(to_float(part.x[i])) : 0.0;
     __syncthreads();
     // ---- scores: 8 pairs x 8 pages a warp and tile; a lane's channels are 16 i + 4 t .. + 3.
-    // The next tile's sums are on their way while this one's are multiplied.
+    // With two blocks an SM the next tile's sums are on their way while this one's are multiplied.
     {
       const int g = lane >> 2, t = lane & 3;
       const int* sums = P.c.ksum + static_cast<size_t>(h) * HD + 4 * t;
@@ -329,13 +367,14 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
 #pragma unroll
         for (int i = 0; i < HD / 16; ++i) v[i] = slot >= 0 ? __ldg(k4 + 4 * i) : make_int4(0, 0, 0, 0);
       };
-      if (warp * 8 < most) fetch(warp * 8);
+      if (!kThree && warp * 8 < most) fetch(warp * 8);
 #pragma unroll 1
       for (int j0 = warp * 8; j0 < most; j0 += kWarps * 8) {
         int4 u[HD / 16];
+        if (kThree) fetch(j0);
 #pragma unroll
         for (int i = 0; i < HD / 16; ++i) u[i] = v[i];
-        if (j0 + kWarps * 8 < most) fetch(j0 + kWarps * 8);
+        if (!kThree && j0 + kWarps * 8 < most) fetch(j0 + kWarps * 8);
         double c[2][2] = {{0.0, 0.0}, {0.0, 0.0}};                   // two chains
 #pragma unroll
         for (int i = 0; i < HD / 16; ++i) {
@@ -362,7 +401,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
       for (int j = lane; j < own; j += 32) mx = fmax(mx, x[j]);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) mx = fmax(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-#pragma unroll 2
+#pragma unroll 4
       for (int j = lane; j < own; j += 32) {
         const double e = exp(x[j] - mx);
         x[j] = e;
@@ -433,9 +472,13 @@ static cudaError_t select_t(SelectParams& P, cudaStream_t st) {
   const long long grid = (static_cast<long long>(P.bt.rows) / P.RU + P.bt.B) * P.c.H;
   if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;
   const int smem = static_cast<int>(select_smem(P.pairs, P.RU, P.G, P.stride));
-  cudaError_t e = cudaFuncSetAttribute(select_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // Three blocks an SM, where they fit and the rows fill more than two on each of 148 SMs: 1,176
+  // blocks of 591 pages 130 us, 137 with two that fetch ahead; 256 blocks of 512 pages 30 and 25 us.
+  const bool three = static_cast<long long>(P.bt.rows) / P.RU * P.c.H > 2 * 148 && smem <= 62 * 1024;
+  auto kernel = three ? select_kernel<T, HD, true> : select_kernel<T, HD, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  select_kernel<T, HD><<<static_cast<unsigned>(grid), kSelThreads, smem, st>>>(P);
+  kernel<<<static_cast<unsigned>(grid), kSelThreads, smem, st>>>(P);
   return cudaGetLastError();
 }
 

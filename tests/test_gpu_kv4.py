@@ -358,6 +358,8 @@ SELECT = [
     ([1000, 0, 300], [5, 0, 2], 2, 2, 64, 64, 1.0, 1, BF16, False),
     ([700], [4], 1, 64, 64, 64, 0.7, 3, BF16, False),
     ([900], [3], 2, 4, 128, 64, 0.3, 100, BF16, True),
+    ([2900, 700], [330, 41], 7, 7, 64, 64, 0.85, 1, BF16, False),   # blocks for three an SM
+    ([600, 410], [100, 20], 5, 15, 128, 64, 0.9, 2, FP32, True),
 ]
 
 
