@@ -362,10 +362,10 @@ __global__ void __launch_bounds__(kSelThreads, kThree ? 3 : 2) select_kernel(con
       const size_t page = static_cast<size_t>(P.c.H) * HD;
       int4 v[HD / 16];
       auto fetch = [&](int j0) {
-        const int slot = j0 + g < most ? slots[j0 + g] : -1;
+        const int slot = j0 + g < most ? slots[j0 + g] : 0;
         const int4* k4 = reinterpret_cast<const int4*>(sums + max(slot, 0) * page);
 #pragma unroll
-        for (int i = 0; i < HD / 16; ++i) v[i] = slot >= 0 ? __ldg(k4 + 4 * i) : make_int4(0, 0, 0, 0);
+        for (int i = 0; i < HD / 16; ++i) v[i] = __ldg(k4 + 4 * i);
       };
       if (!kThree && warp * 8 < most) fetch(warp * 8);
 #pragma unroll 1
@@ -385,10 +385,12 @@ __global__ void __launch_bounds__(kSelThreads, kThree ? 3 : 2) select_kernel(con
           mma_f64(c[0], a1.x, static_cast<double>(u[i].z));
           mma_f64(c[1], a1.y, static_cast<double>(u[i].w));
         }
-        // an invalid page (recorded) scores 0; the row of scores is padded to whole tiles
+        // An invalid page (recorded; some page's sums were read in its place) scores 0. The row of
+        // scores and the slots are padded to whole tiles.
+        const int2 from = *reinterpret_cast<const int2*>(&slots[j0 + 2 * t]);
         if (g < NP)
           *reinterpret_cast<double2*>(&xs[static_cast<size_t>(g) * LD + j0 + 2 * t]) =
-              make_double2((c[0][0] + c[1][0]) * w, (c[0][1] + c[1][1]) * w);
+              make_double2(from.x >= 0 ? (c[0][0] + c[1][0]) * w : 0.0, from.y >= 0 ? (c[0][1] + c[1][1]) * w : 0.0);
       }
     }
     __syncthreads();
@@ -473,7 +475,7 @@ static cudaError_t select_t(SelectParams& P, cudaStream_t st) {
   if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;
   const int smem = static_cast<int>(select_smem(P.pairs, P.RU, P.G, P.stride));
   // Three blocks an SM, where they fit and the rows fill more than two on each of 148 SMs: 1,176
-  // blocks of 591 pages 130 us, 137 with two that fetch ahead; 256 blocks of 512 pages 30 and 25 us.
+  // blocks of 591 pages 130 us, 136 with two that fetch ahead; 256 blocks of 512 pages 30 and 25 us.
   const bool three = static_cast<long long>(P.bt.rows) / P.RU * P.c.H > 2 * 148 && smem <= 62 * 1024;
   auto kernel = three ? select_kernel<T, HD, true> : select_kernel<T, HD, false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
