@@ -191,7 +191,9 @@ __global__ void __launch_bounds__(kWriteThreads, sizeof(T) == 2 ? 4 : 3)
   const int n = held(kv_len[b], bt, block, status);
   const int start = n - q;                    // position of row r0
   if (start < 0 && threadIdx.x == 0) record_status(status, FVATTN_ERR_INVALID_ARG);
-  const int pg = max(start, 0) / block + tile - (r0 / block + 2 * b);
+  const int nth = tile - (r0 / block + 2 * b);   // of the pages that the rows touch
+  if (nth < 0) return;                        // a tile of the rows before cu[0]
+  const int pg = max(start, 0) / block + nth;
   const int first = max(start, pg * block);   // positions [first, last) of this block
   const int last = min(min(n, (pg + 1) * block), start + bt.rows - r0);   // rows of the tensors only
   if (first >= last) return;

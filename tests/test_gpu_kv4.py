@@ -723,6 +723,30 @@ def test_odd_row_starts(cu):
         c.assert_records(before)                            # what was read is what is written again
 
 
+@pytest.mark.parametrize("block", [64, 128])
+def test_more_rows_than_tokens_behind_rows_of_no_sequence(block):
+    """A first sequence that starts at row 260 and has more rows than tokens: the tiles of the rows before it
+    touch no page (the entries in front of its table row are valid slots here, which would be written)."""
+    c = Case([block + 9], [4], 2, 64, block, seed=60)
+    wide = torch.arange(5 * c.max_pages, dtype=torch.int32, device="cuda").reshape(5, -1) % c.cache.num_pages
+    wide[4] = c.table[0].clamp(min=0)
+    one = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    rows, kv = 3 * block, 5
+    b = F.KV4Batch(wide[4:], one(kv), one(260, 260 + rows), rows)
+    k, v = (torch.randn((260 + rows + 9, 2, 64), generator=c.g).to(BF16) for _ in range(2))
+    want = c.records()
+    for i, x in enumerate((k, v)):                          # the last five rows are the tokens held
+        codes, scales = O.quantize(x[260 + rows - kv:260 + rows].float().numpy())
+        for w, y in ((want[2 * i], codes), (want[2 * i + 1], scales)):
+            w[c.table_np[0, 0], :, :kv] = y.transpose(1, 0, 2)
+    sums = c.cache.ksum.clone()
+    ws = c.ws(F.FVATTN_OP_KV4_APPEND, len(k), b)
+    F.fvattn_kv4_append(c.cache, b, k.cuda(), v.cuda(), ws)
+    assert F.fvattn_workspace_status(ws) == F.FVATTN_ERR_INVALID_ARG
+    c.assert_records(want)
+    assert torch.equal(sums, c.cache.ksum)
+
+
 def test_rewriting_what_was_read_changes_nothing():
     """Quantizing stored values gives them back: codes, scales and sums."""
     c = Case([200, 130], [200, 130], 2, 128, 64, seed=49)
