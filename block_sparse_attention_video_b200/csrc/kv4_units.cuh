@@ -124,6 +124,10 @@ struct Entries {
       }
       b = lo;
       if (r < cu[b]) return 0;                  // before the first sequence
+      if (cu[b] < 0) {                          // r - cu[b] has no bound then
+        record_status(P.status, FVATTN_ERR_INVALID_ARG);
+        return 0;
+      }
       if (cnt < 0 || cnt > P.bt.max_pages) {
         record_status(P.status, FVATTN_ERR_INVALID_ARG);
         cnt = min(max(cnt, 0), P.bt.max_pages);

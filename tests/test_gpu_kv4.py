@@ -723,6 +723,23 @@ def test_odd_row_starts(cu):
         c.assert_records(before)                            # what was read is what is written again
 
 
+@pytest.mark.parametrize("start", [-1, -77, -(1 << 28), -(1 << 30), -(1 << 31)])
+@pytest.mark.parametrize("G", [1, 8])
+def test_negative_row_starts_with_lists(start, G):
+    """The sequence is skipped and recorded, however far below 0 its start is (times G it has no 32-bit value)."""
+    c = Case([300, 200], [3, 2], 1, 64, 64, seed=61, Hq=G)
+    q = c.make_q()
+    idx = torch.zeros((5, 1, c.max_pages), dtype=torch.int32, device="cuda")
+    idx[:, 0, :2] = torch.tensor([1, 2], dtype=torch.int32)
+    cnt = torch.full((5, 1), 2, dtype=torch.int32, device="cuda")
+    c.batch.cu[0] = start
+    out, lse = c.attend(q, True, idx, cnt)
+    assert F.fvattn_workspace_status(c.last_ws) == F.FVATTN_ERR_INVALID_ARG
+    assert torch.all(out[:3] == 77) and torch.all(lse[:3] == 77)
+    c.kv, c.nrow, c.k, c.v = c.kv[1:], [2], c.k[1:], c.v[1:]
+    c.check(q[3:], out[3:], lse[3:], lists=[[[1, 2]], [[1, 2]]])
+
+
 @pytest.mark.parametrize("block", [64, 128])
 def test_more_rows_than_tokens_behind_rows_of_no_sequence(block):
     """A first sequence that starts at row 260 and has more rows than tokens: the tiles of the rows before it
