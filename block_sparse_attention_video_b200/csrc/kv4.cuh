@@ -59,7 +59,8 @@ __device__ __forceinline__ void record_status(const Status& s, int code) {
   }
 }
 
-// A sequence's length n, clamped to what its table row can hold.
+// A sequence's length n, clamped to what its table row can hold. Positions count from the length
+// itself (start_of): a row behind the table's end is left out, the others stay where they are.
 __device__ __forceinline__ int held(int n, const Batch& bt, int block, const Status& status) {
   const int most = bt.max_pages * block;
   if (n < 0 || n > most) {
@@ -68,6 +69,9 @@ __device__ __forceinline__ int held(int n, const Batch& bt, int block, const Sta
   }
   return n;
 }
+
+// Position of the first of a sequence's q >= 0 rows, of n tokens.
+__device__ __forceinline__ int start_of(int n, int q) { return max(n, 0) - q; }
 
 // Pool slot of page pg (in [0, max_pages)) of sequence b; -1 (recorded) if invalid.
 __device__ __forceinline__ int pool_slot(const Batch& bt, int num_pages, int b, int pg, const Status& status) {

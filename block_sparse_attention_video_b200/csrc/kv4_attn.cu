@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : sizeof(T) == 4 ? 1 : 2
     if (fresh) {                                   // Q comes while the first pages are on their way
       if (!warp_wait(&sm.unit_full[units & 1], (units >> 1) & 1, abort_flag, P.status)) return;
       fresh = false;
-      const int mc = m.mc, m0 = m.m0, h = m.h, cu = m.cu, nq = m.q, n = m.n;
+      const int mc = m.mc, m0 = m.m0, h = m.h, cu = m.cu, start = m.start, n = m.n;
       const float base = P.scale_log2 * (P.c.k_scale ? __ldg(P.c.k_scale + h) : 1.f);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : sizeof(T) == 4 ? 1 : 2
           const int e = __shfl_sync(0xffffffffu, ex, col * 4);
           // never 0: a masked key's -inf times it has to stay -inf
           cs[j][y] = fmaxf(base * exp2f(static_cast<float>(-(e / 2))) * exp2f(static_cast<float>(-(e - e / 2))), FLT_MIN);
-          const int pos = n - nq + (m0 + c_row) / P.G;
+          const int pos = start + (m0 + c_row) / P.G;
           see[j][y] = c_row < mc ? (P.causal ? min(max(pos + 1, 0), n) : n) : 0;
           mref[j][y] = kFloor;
           l[j][y] = 0.f;

@@ -433,7 +433,7 @@ __device__ void softmax(const AttnParams& P, Smem<HD>& sm, uint32_t tmem) {
       // never 0, so that a masked key's -inf stays -inf
       cs = fmaxf(base * exp2f(static_cast<float>(-(ex / 2))) * exp2f(static_cast<float>(-(ex - ex / 2))), FLT_MIN);
       const int n = m.n;
-      left = (live ? (P.causal ? min(max(n - m.q + i_row + 1, 0), n) : n) : 0) - m.s0 * kStep;
+      left = (live ? (P.causal ? min(max(m.start + i_row + 1, 0), n) : n) : 0) - m.s0 * kStep;
     }
     float mref = kFloor, l_run = 0.f;
 #pragma unroll 1

@@ -330,12 +330,13 @@ __global__ void __launch_bounds__(kSelThreads, kThree ? 3 : 2) select_kernel(con
   if (r0 < 0 && tid == 0) record_status(P.status, FVATTN_ERR_INVALID_ARG);
   if (r0 < 0 || first < r0 || rows <= 0) return;
   const int n = held(kv_len[b], P.bt, P.block, P.status);
-  const int pos0 = n - (r1 - first);                                 // position of the first row
-  const int most = pos0 + rows - 1 < 0 ? 0 : (pos0 + rows - 1) / P.block;   // pages to score
+  const int pos0 = start_of(kv_len[b], r1 - first);                  // position of the first row
+  const int last = min(pos0 + rows, n) - 1;                          // last position of the group
+  const int most = last < 0 ? 0 : last / P.block;                    // pages to score
   const double w = P.w * (P.c.k_scale ? static_cast<double>(__ldg(P.c.k_scale + h)) : 1.0);
   const int chunks = (G + NP - 1) / NP;                              // of query heads; one if RU > 1
-  // Pages that row i of the group scores; 0 for a row before the sequence (recorded below).
-  auto own_of = [&](int i) { return i < rows && pos0 + i >= 0 ? (pos0 + i) / P.block : 0; };
+  // Pages that row i of the group scores; 0 for a row outside the sequence (recorded below).
+  auto own_of = [&](int i) { return i < rows && pos0 + i >= 0 && pos0 + i < n ? (pos0 + i) / P.block : 0; };
   for (int ch = 0; ch < chunks; ++ch) {
     // pair k: row k / G, head k % G (RU rows), or head ch * NP + k of the one row
     auto row_of = [&](int k) { return RU > 1 ? k / G : 0; };
@@ -446,9 +447,9 @@ __global__ void __launch_bounds__(kSelThreads, kThree ? 3 : 2) select_kernel(con
     const int own = own_of(i);
     if (own == 0) {
       if (lane == 0) {
-        const bool before = pos0 + i < 0;
-        if (before) record_status(P.status, FVATTN_ERR_INVALID_ARG); else out[0] = 0;
-        P.kv_cnt[unit] = before ? 0 : 1;
+        const bool outside = pos0 + i < 0 || pos0 + i >= n;
+        if (outside) record_status(P.status, FVATTN_ERR_INVALID_ARG); else out[0] = 0;
+        P.kv_cnt[unit] = outside ? 0 : 1;
       }
       continue;
     }

@@ -56,12 +56,12 @@ struct AttnParams {
 // A unit, as its producer publishes it to the other warps.
 struct alignas(16) Meta {
   int cu, q, n;           // the sequence: first row, rows, tokens held
+  int start;              // position of its first row
   int m0, mc;             // first (row, head) pair and their number
   int h;                  // KV head
   int seen;               // keys that the unit's last row sees
   int begin, end;         // blocks that hold the unit's first and last step
   int s0, ns;             // first of the unit's steps in this block, and their number
-  int pad;
 };
 
 // First rows and lengths of the sequences, copied to shared memory where they are few: the
@@ -109,6 +109,8 @@ struct Entries {
     return P.kv_idx ? static_cast<long long>(P.bt.rows) * P.c.H
                     : static_cast<long long>(P.bt.rows) * P.G / RT + P.bt.B;
   }
+  // start_of, at most the table's end: a row there or behind it sees every token held.
+  __device__ int start(int n, int q) const { return min(start_of(n, q), P.bt.max_pages * P.block); }
   __device__ int times() const { return P.kv_idx ? (P.G + RT - 1) / RT : P.c.H; }
   // Steps of a unit of entry e and where it lies; 0 if the entry is not in use.
   __device__ int steps(long long e, int& b, int& m0, int& seen, Meta* m) const {
@@ -137,7 +139,8 @@ struct Entries {
         m->cu = cu[b];
         m->q = cu[b + 1] - m->cu;
         m->n = held(kv_len[b], P.bt, P.block, P.status);
-        const int pos = m->n - m->q + (r - m->cu);
+        m->start = start(kv_len[b], m->q);
+        const int pos = m->start + (r - m->cu);
         seen = P.causal ? min(max(pos + 1, 0), m->n) : m->n;
       }
       return max(1, (cnt * P.block + kStep - 1) / kStep);
@@ -156,11 +159,13 @@ struct Entries {
     m0 = static_cast<int>(first);
     const int n = held(kv_len[b], P.bt, P.block, P.status);
     const int last = min((m0 + RT - 1) / P.G, q - 1);
-    seen = P.causal ? min(max(n - (r1 - r0) + last + 1, 0), n) : n;
+    const int pos0 = start(kv_len[b], r1 - r0);
+    seen = P.causal ? min(max(pos0 + last + 1, 0), n) : n;
     if (m) {
       m->cu = r0;
       m->q = r1 - r0;
       m->n = n;
+      m->start = pos0;
     }
     return max(1, (seen + kStep - 1) / kStep);
   }

@@ -189,8 +189,9 @@ __global__ void __launch_bounds__(kWriteThreads, sizeof(T) == 2 ? 4 : 3)
   if (r0 < 0 && threadIdx.x == 0) record_status(status, FVATTN_ERR_INVALID_ARG);
   if (q <= 0 || r0 < 0) return;
   const int n = held(kv_len[b], bt, block, status);
-  const int start = n - q;                    // position of row r0
+  const int start = start_of(kv_len[b], q);   // position of row r0
   if (start < 0 && threadIdx.x == 0) record_status(status, FVATTN_ERR_INVALID_ARG);
+  if (start >= n) return;                     // all behind the table's end (recorded above)
   const int nth = tile - (r0 / block + 2 * b);   // of the pages that the rows touch
   if (nth < 0) return;                        // a tile of the rows before cu[0]
   const int pg = max(start, 0) / block + nth;
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(kWriteThreads)
       }
       const int b = lo;
       if (r >= cu[b]) {
-        const int n = held(kv_len[b], bt, block, status), pos = n - (cu[b + 1] - r);
+        const int n = held(kv_len[b], bt, block, status), pos = start_of(kv_len[b], cu[b + 1] - r);
         slot = -1;
         if (pos >= 0 && pos < n) slot = pool_slot(bt, c.num_pages, b, pos / block, status);
         else record_status(status, FVATTN_ERR_INVALID_ARG);

@@ -723,6 +723,61 @@ def test_odd_row_starts(cu):
         c.assert_records(before)                            # what was read is what is written again
 
 
+@pytest.mark.parametrize("rows,over", [(1, 1), (5, 2), (70, 1), (70, 70), (3, 40), (2, (1 << 31) - 1 - 256)])
+@pytest.mark.parametrize("block", [64, 128])
+def test_longer_than_the_table_row(rows, over, block):
+    """Rows keep their positions where a sequence is longer than its table row holds: those behind it are not
+    written, read as zeros and choose no page; what is held stays as it is."""
+    cap = 256
+    c = Case([cap, 90], [rows, 1], 2, 64, block, seed=62, Hq=4)
+    c.max_pages = cap // block
+    c.table = c.table[:, :c.max_pages].clamp(min=0).contiguous()
+    c.batch = c.batch_of([rows, 1], [cap + over, 90])
+    fits = max(0, rows - over)                              # rows at positions below cap
+    bad = lambda ws: F.fvattn_workspace_status(ws) == F.FVATTN_ERR_INVALID_ARG
+    want = c.records()
+    k, v = (torch.randn((rows + 1, 2, 64), generator=c.g).to(BF16) for _ in range(2))
+    for mine, new in ((c.k, k), (c.v, v)):
+        mine[0][cap - fits:] = new[:fits]
+        mine[1][89] = new[rows]
+    places = [(0, t) for t in range(cap - fits, cap)] + [(1, 89)]
+    parts = [c.quantized(b) for b in range(2)]
+    for b, t in places:
+        for w, x in zip(want, parts[b]):
+            w[c.table_np[b, t // block], :, t % block] = x[t]
+    ws = c.ws(F.FVATTN_OP_KV4_APPEND, rows + 1)
+    F.fvattn_kv4_append(c.cache, c.batch, k.cuda(), v.cuda(), ws)
+    assert bad(ws)
+    c.assert_records(want)
+    ksum, plain = c.cache.ksum.cpu().numpy(), O.dequantize(*parts[0][:2])
+    for pg in range(cap // block):
+        for h in range(2):
+            assert np.array_equal(ksum[c.table_np[0, pg], h], O.page_sum(plain[pg * block:(pg + 1) * block, h]))
+    ko, vo = (torch.full((rows + 1, 2, 64), 5.0, device="cuda") for _ in range(2))
+    F.fvattn_kv4_read(c.cache, c.batch, ko, vo, ws)
+    assert bad(ws) and not ko[fits:rows].any() and not vo[fits:rows].any()
+    for got, x in ((ko, 0), (vo, 1)):
+        assert np.array_equal(got[:fits].cpu().numpy(), c.values(0)[x][cap - fits:])
+        assert np.array_equal(got[rows].cpu().numpy(), c.values(1)[x][89])
+    q = c.make_q(spread=4.0)
+    live = list(range(fits)) + [rows]
+    idx, cnt = _select(c, q, 0.8, 1)
+    assert bad(c.last_ws) and not cnt[fits:rows].any()
+    lists = idx[:, :, :1].new_zeros((rows + 1, 2, c.max_pages)) + torch.arange(c.max_pages, device="cuda").int()
+    full = torch.full((rows + 1, 2), c.max_pages, dtype=torch.int32, device="cuda")
+    full[rows] = 2
+    outs = [c.attend(q), c.attend(q, True, lists, full)]
+    assert bad(c.last_ws)
+    c.nrow = [fits, 1]
+    got = [[idx[r, h, :cnt[r, h]].tolist() for h in range(2)] for r in live]
+    assert got == _want_lists(c, q[live], 0.8, 1)
+    for out, lse in outs:
+        c.nrow = [fits, 1]
+        c.check(q[live], out[live], lse[live])
+        c.nrow = [rows - fits, 0]                           # behind the end: all that is held
+        c.check(q[fits:rows], out[fits:rows], lse[fits:rows], causal=False)
+
+
 @pytest.mark.parametrize("start", [-1, -77, -(1 << 28), -(1 << 30), -(1 << 31)])
 @pytest.mark.parametrize("G", [1, 8])
 def test_negative_row_starts_with_lists(start, G):
