@@ -70,6 +70,18 @@ __device__ __forceinline__ int held(int n, const Batch& bt, int block, const Sta
   return n;
 }
 
+// Where the call's rows end: those behind belong to no sequence.
+__device__ __forceinline__ int rows_end(const Batch& bt, const int* cu) { return min(cu[bt.B], bt.rows); }
+
+// Records row starts that are negative or fall, and an end outside the tensors; by one block, all its
+// threads. cu: bt.cu or a copy.
+__device__ __forceinline__ void check_rows(const Batch& bt, const int* cu, const Status& status) {
+  if (blockIdx.x != 0) return;
+  bool bad = threadIdx.x == 0 && (cu[bt.B] < 0 || cu[bt.B] > bt.rows);
+  for (int b = threadIdx.x; b < bt.B; b += blockDim.x) bad |= cu[b] < 0 || (b + 1 < bt.B && cu[b + 1] < cu[b]);
+  if (bad) record_status(status, FVATTN_ERR_INVALID_ARG);
+}
+
 // Position of the first of a sequence's q >= 0 rows, of n tokens.
 __device__ __forceinline__ int start_of(int n, int q) { return max(n, 0) - q; }
 

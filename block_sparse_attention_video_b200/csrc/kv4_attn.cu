@@ -146,7 +146,7 @@ __device__ void produce(const AttnParams& P, AttnSmem<HD, NT>& sm) {
       m.h = which;
       m.m0 = m0;
       m.mc = static_cast<int>(
-          min(static_cast<long long>(RT), static_cast<long long>(min(m.q, P.bt.rows - m.cu)) * P.G - m0));
+          min(static_cast<long long>(RT), static_cast<long long>(m.q) * P.G - m0));
       cnt = (seen + P.block - 1) / P.block;
     }
     m.seen = seen;

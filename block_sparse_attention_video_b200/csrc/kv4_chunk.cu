@@ -144,8 +144,7 @@ __device__ void produce(const AttnParams& P, Smem<HD>& sm) {
       }
       m.h = which;
       m.m0 = m0;
-      m.mc = static_cast<int>(min(static_cast<long long>(kRows),
-                                  static_cast<long long>(min(m.q, P.bt.rows - m.cu)) * P.G - m0));
+      m.mc = static_cast<int>(min(static_cast<long long>(kRows), static_cast<long long>(m.q) * P.G - m0));
       m.seen = seen;
       m.ns = static_cast<int>(min(static_cast<long long>(steps - m.s0), hi - x));
       m.begin = piece_of(x - m.s0, total, sm.piece.blocks);

@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kSelThreads, kThree ? 3 : 2) select_kernel(con
   seqs.load<kSelThreads>(P.bt);
   __syncthreads();
   const int *cu = seqs.rows_of(P.bt), *kv_len = seqs.lengths_of(P.bt);
-  if (blockIdx.x == 0 && tid == 0 && cu[P.bt.B] > P.bt.rows) record_status(P.status, FVATTN_ERR_INVALID_ARG);
+  check_rows(P.bt, cu, P.status);
   // Groups are numbered without a prefix sum: sequence b owns those from cu[b]/RU + b on.
   const int h = blockIdx.x % P.c.H, tile = blockIdx.x / P.c.H;
   int lo = 0, hi = P.bt.B;
@@ -326,8 +326,7 @@ __global__ void __launch_bounds__(kSelThreads, kThree ? 3 : 2) select_kernel(con
   }
   const int b = lo, r0 = cu[b], r1 = cu[b + 1];
   const int first = r0 + (tile - (r0 / RU + b)) * RU;                // first row of the group
-  const int rows = min(RU, min(r1, P.bt.rows) - first);
-  if (r0 < 0 && tid == 0) record_status(P.status, FVATTN_ERR_INVALID_ARG);
+  const int rows = min(RU, min(r1, rows_end(P.bt, cu)) - first);
   if (r0 < 0 || first < r0 || rows <= 0) return;
   const int n = held(kv_len[b], P.bt, P.block, P.status);
   const int pos0 = start_of(kv_len[b], r1 - first);                  // position of the first row

@@ -55,7 +55,7 @@ struct AttnParams {
 
 // A unit, as its producer publishes it to the other warps.
 struct alignas(16) Meta {
-  int cu, q, n;           // the sequence: first row, rows, tokens held
+  int cu, q, n;           // the sequence: first row, rows (of the tensors), tokens held
   int start;              // position of its first row
   int m0, mc;             // first (row, head) pair and their number
   int h;                  // KV head
@@ -125,11 +125,7 @@ struct Entries {
         if (cu[mid] <= r) lo = mid; else hi = mid;
       }
       b = lo;
-      if (r < cu[b]) return 0;                  // before the first sequence
-      if (cu[b] < 0) {                          // r - cu[b] has no bound then
-        record_status(P.status, FVATTN_ERR_INVALID_ARG);
-        return 0;
-      }
+      if (cu[b] < 0 || r < cu[b]) return 0;     // skipped (r - cu[b] has no bound), or before the first
       if (cnt < 0 || cnt > P.bt.max_pages) {
         record_status(P.status, FVATTN_ERR_INVALID_ARG);
         cnt = min(max(cnt, 0), P.bt.max_pages);
@@ -152,9 +148,8 @@ struct Entries {
     }
     b = lo;
     const int r0 = cu[b], r1 = cu[b + 1];
-    const int q = min(r1, P.bt.rows) - r0;
+    const int q = min(r1, rows_end(P.bt, cu)) - r0;
     const long long first = (e - (static_cast<long long>(r0) * P.G / RT + b)) * RT;
-    if (r0 < 0) record_status(P.status, FVATTN_ERR_INVALID_ARG);
     if (r0 < 0 || q <= 0 || first < 0 || first >= static_cast<long long>(q) * P.G) return 0;
     m0 = static_cast<int>(first);
     const int n = held(kv_len[b], P.bt, P.block, P.status);
@@ -163,7 +158,7 @@ struct Entries {
     seen = P.causal ? min(max(pos0 + last + 1, 0), n) : n;
     if (m) {
       m->cu = r0;
-      m->q = r1 - r0;
+      m->q = q;
       m->n = n;
       m->start = pos0;
     }
@@ -186,7 +181,7 @@ __device__ void find_piece(const AttnParams& P, Seqs& seqs, Piece& sm, int least
   seqs.load<kThreads>(P.bt);
   __syncthreads();
   const Entries<RT> en(P, seqs);
-  if (blockIdx.x == 0 && threadIdx.x == 0 && en.cu[P.bt.B] > P.bt.rows) record_status(P.status, FVATTN_ERR_INVALID_ARG);
+  check_rows(P.bt, en.cu, P.status);
   const long long E = en.count();
   const int mult = en.times();
   const long long chunk = (E + kThreads - 1) / kThreads;

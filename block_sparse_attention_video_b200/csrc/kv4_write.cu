@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kWriteThreads, sizeof(T) == 2 ? 4 : 3)
   const int *cu = seqs.rows_of(bt), *kv_len = seqs.lengths_of(bt);
   const int h = blockIdx.x % c.H;
   const int tile = blockIdx.x / c.H;
-  if (blockIdx.x == 0 && threadIdx.x == 0 && cu[bt.B] > bt.rows) record_status(status, FVATTN_ERR_INVALID_ARG);
+  check_rows(bt, cu, status);
   int lo = 0, hi = bt.B;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -186,7 +186,6 @@ __global__ void __launch_bounds__(kWriteThreads, sizeof(T) == 2 ? 4 : 3)
   const int b = lo;
   const int r0 = cu[b];
   const int q = cu[b + 1] - r0;
-  if (r0 < 0 && threadIdx.x == 0) record_status(status, FVATTN_ERR_INVALID_ARG);
   if (q <= 0 || r0 < 0) return;
   const int n = held(kv_len[b], bt, block, status);
   const int start = start_of(kv_len[b], q);   // position of row r0
@@ -196,7 +195,7 @@ __global__ void __launch_bounds__(kWriteThreads, sizeof(T) == 2 ? 4 : 3)
   if (nth < 0) return;                        // a tile of the rows before cu[0]
   const int pg = max(start, 0) / block + nth;
   const int first = max(start, pg * block);   // positions [first, last) of this block
-  const int last = min(min(n, (pg + 1) * block), start + bt.rows - r0);   // rows of the tensors only
+  const int last = min(min(n, (pg + 1) * block), start + rows_end(bt, cu) - r0);
   if (first >= last) return;
   const int slot = pool_slot(bt, c.num_pages, b, pg, status);
   if (slot < 0) return;
@@ -293,7 +292,7 @@ __global__ void __launch_bounds__(kWriteThreads)
   seqs.load<kWriteThreads>(bt);
   __syncthreads();
   const int *cu = seqs.rows_of(bt), *kv_len = seqs.lengths_of(bt);
-  if (blockIdx.x == 0 && threadIdx.x == 0 && cu[bt.B] > bt.rows) record_status(status, FVATTN_ERR_INVALID_ARG);
+  check_rows(bt, cu, status);
   const unsigned H = static_cast<unsigned>(c.H), u0 = blockIdx.x * UNITS;
   const unsigned row0 = u0 / H, rows = min(u0 + UNITS - 1, bt.rows * H - 1) / H - row0 + 1;
   for (unsigned i = threadIdx.x; i < rows; i += kWriteThreads) {
@@ -306,7 +305,7 @@ __global__ void __launch_bounds__(kWriteThreads)
         if (cu[mid] <= r) lo = mid; else hi = mid;
       }
       const int b = lo;
-      if (r >= cu[b]) {
+      if (cu[b] >= 0 && r >= cu[b]) {
         const int n = held(kv_len[b], bt, block, status), pos = start_of(kv_len[b], cu[b + 1] - r);
         slot = -1;
         if (pos >= 0 && pos < n) slot = pool_slot(bt, c.num_pages, b, pos / block, status);

@@ -431,11 +431,12 @@ typedef struct {
  * All three arrays are device memory and are read when the call's kernels run, so lengths
  * may change between the replays of a captured call. What they hold is checked there, each
  * element where it is used: a position outside [0, max_pages*block), a pool slot outside
- * [0, num_pages), cu[b] < 0 or cu[B] > rows is skipped or clamped and recorded as
- * FVATTN_ERR_INVALID_ARG in the workspace. Where kv_len[b] is more than a table row holds, the rows
- * keep their positions: those behind the table's end are not written, read as zeros and choose no
- * page, and in the attention see every token that the table row holds. A sequence may have no rows.
- * Two sequences may share pages that no row of the call writes.                          */
+ * [0, num_pages), a sequence with cu[b] < 0 or cu[B] outside [0, rows] is skipped or clamped and
+ * recorded as FVATTN_ERR_INVALID_ARG in the workspace. A start cu[b] (b < B) below the one before it
+ * is recorded too, and the rows that two sequences then claim get unspecified results. Where kv_len[b]
+ * is more than a table row holds, the rows keep their positions: those behind the table's end are not
+ * written, read as zeros and choose no page, and in the attention see every token that the table row
+ * holds. A sequence may have no rows. Two sequences may share pages that no row of the call writes. */
 typedef struct {
   const int32_t* table;    /* device [B][max_pages] pool slots                            */
   const int32_t* kv_len;   /* device [B] tokens held                                      */

@@ -723,6 +723,66 @@ def test_odd_row_starts(cu):
         c.assert_records(before)                            # what was read is what is written again
 
 
+@pytest.mark.parametrize("cu,good", [([2, 4, 4, 5], True), ([0, 1, 4, 2], True), ([0, 4, 2, 6], False),
+                                     ([-3, 1, 2, 4], False), ([0, 3, 3, 900], False), ([0, 2, 4, -1], False)])
+def test_the_calls_agree_on_the_rows(cu, good):
+    """All four calls, on both attention kernels and over lists: rows in front of cu[0], of a sequence with a
+    negative start and from cu[B] on are left alone, others get their own sequence's results, and starts that
+    are negative or fall are recorded."""
+    n = 7
+    c = Case([300, 200, 150], [1, 1, 1], 1, 64, 64, seed=63, Hq=2)
+    kv, k, v = c.kv, c.k, c.v
+    ok = lambda ws: (F.fvattn_workspace_status(ws) == F.FVATTN_OK) == good
+    owners = [[b for b in range(3) if 0 <= cu[b] <= r < min(cu[b + 1], cu[3])] for r in range(n)]
+    free = [r for r in range(n) if not owners[r]]
+    sole = [(r, o[0], kv[o[0]] - (cu[o[0] + 1] - r)) for r, o in enumerate(owners) if len(o) == 1]
+    assert free or cu[3] > n
+    q = torch.randn((n, 2, 64), generator=c.g).to(BF16)
+    lists = torch.arange(c.max_pages, dtype=torch.int32, device="cuda").expand(n, 1, -1).contiguous()
+    for max_q in (1, 300):
+        c.batch = F.KV4Batch(c.table, c.batch.kv_len, torch.tensor(cu, dtype=torch.int32, device="cuda"), max_q)
+        runs = [c.attend(q)]
+        assert ok(c.last_ws)
+        cnt = torch.ones((n, 1), dtype=torch.int32, device="cuda")
+        for r, b, pos in sole:
+            cnt[r] = pos // 64 + 1
+        runs.append(c.attend(q, True, lists, cnt))
+        assert ok(c.last_ws)
+        for out, lse in runs:
+            assert torch.all(out[free] == 77) and torch.all(lse[free] == 77)
+            for r, b, pos in sole:
+                c.kv, c.nrow = [pos + 1 if i == b else 0 for i in range(3)], [int(i == b) for i in range(3)]
+                c.check(q[r:r + 1], out[r:r + 1], lse[r:r + 1])
+    idx, cnt = _select(c, q, 0.8, 1)
+    assert ok(c.last_ws) and torch.all(cnt[free] == -5) and torch.all(idx[free] == -5)
+    for r, b, pos in sole:
+        c.kv, c.nrow = [pos + 1 if i == b else 0 for i in range(3)], [int(i == b) for i in range(3)]
+        c.k = [x[:max(m, 0)] for x, m in zip(k, c.kv)]
+        want = _want_lists(c, q[r:r + 1], 0.8, 1)[0] if pos >= 0 else [[]]      # in front of the sequence: none
+        assert [idx[r, 0, :cnt[r, 0]].tolist()] == want
+    c.k = k
+    ws = c.ws(F.FVATTN_OP_KV4_READ, n)
+    ko, vo = (torch.full((n, 1, 64), 5.0, device="cuda") for _ in range(2))
+    F.fvattn_kv4_read(c.cache, c.batch, ko, vo, ws)
+    assert ok(ws) and torch.all(ko[free] == 5) and torch.all(vo[free] == 5)
+    for r, b, pos in sole:
+        assert all(np.array_equal(x[r].cpu().numpy(), y[pos] if pos >= 0 else 0 * y[0])
+                   for x, y in zip((ko, vo), c.values(b)))
+    want = c.records()
+    new = torch.randn((n, 1, 64), generator=c.g)
+    codes, scales = O.quantize(new.numpy())
+    for r, o in enumerate(owners):                          # (a row that two claim is written for each)
+        for b in o:
+            pos = kv[b] - (cu[b + 1] - r)
+            if pos < 0:
+                continue
+            for i, x in enumerate((codes, scales, codes, scales)):
+                want[i][c.table_np[b, pos // 64], :, pos % 64] = x[r]
+    F.fvattn_kv4_append(c.cache, c.batch, new.cuda(), new.cuda(), ws)
+    assert ok(ws)
+    c.assert_records(want)
+
+
 @pytest.mark.parametrize("rows,over", [(1, 1), (5, 2), (70, 1), (70, 70), (3, 40), (2, (1 << 31) - 1 - 256)])
 @pytest.mark.parametrize("block", [64, 128])
 def test_longer_than_the_table_row(rows, over, block):
