@@ -230,6 +230,12 @@ class KV4Path:
 
     def __init__(self, cache: KV4Cache, H_q, max_rows, max_batch, max_pages, dtype, p=None, k_min=1, causal=True,
                  scale=None):
+        if p is not None and not 0.0 < p <= 1.0:
+            raise ValueError(f"p = {p} is not in (0, 1]")
+        if int(k_min) < 1:
+            raise ValueError("k_min must be positive")
+        if scale is not None and not 0.0 < scale < math.inf:
+            raise ValueError("scale must be positive and finite")
         self.cache, self.H_q, self.p, self.k_min, self.causal, self.scale = cache, int(H_q), p, int(k_min), causal, scale
         self.max_rows, self.max_batch, self.max_pages = int(max_rows), int(max_batch), int(max_pages)
         dev = cache.device
@@ -256,10 +262,20 @@ class KV4Path:
         if rows > self.max_rows or batch.B > self.max_batch or batch.max_pages != self.max_pages:
             raise ValueError(f"{rows} rows of {batch.B} sequences with {batch.max_pages} pages do not fit the path "
                              f"({self.max_rows}, {self.max_batch}, {self.max_pages})")
-        # all of it before the first call writes into the cache
+        # all of it before the first call writes into the cache (which looks at k and v itself)
         if q.shape[1:] != self.out.shape[1:] or q.dtype != self.out.dtype:
             raise ValueError(f"q is {tuple(q.shape)} {q.dtype}, the path's rows are {tuple(self.out.shape[1:])} "
                              f"{self.out.dtype}")
+        _, heads, stride, _ = _rows(q, "q", self.cache.device, self.H_q, self.cache.d)
+        at, es, row = q.data_ptr(), q.element_size(), heads * self.cache.d
+        if at % 16:
+            raise ValueError("q must be 16-byte aligned")
+        if at < self.out.data_ptr() + rows * row * es and self.out.data_ptr() < at + ((rows - 1) * stride + row) * es:
+            raise ValueError("q overlaps the path's output")
+        if batch.max_q > self.max_rows:              # more rows than there are: the attention's kernel for many may need more
+            need = fvattn_kv4_workspace_bytes(FVATTN_OP_KV4_ATTN, self.cache, batch, rows, self.H_q)
+            if need > self.ws_attn.numel():
+                raise ValueError(f"the batch's max_q {batch.max_q} does not fit the path's {self.max_rows} rows")
         if k.shape[0] != rows or v.shape[0] != rows:
             raise ValueError(f"q has {rows} rows, k {k.shape[0]} and v {v.shape[0]}")
         fvattn_kv4_append(self.cache, batch, k, v, self.ws_append)

@@ -1059,6 +1059,31 @@ def test_the_path_refuses_before_it_writes():
     assert torch.equal(before, c.cache.pages)
 
 
+def test_the_path_refuses_layouts_and_sizes_before_it_writes():
+    c = Case([100, 60], [1, 1], 2, 64, 64, seed=64, Hq=4)
+    make = lambda **kw: F.KV4Path(c.cache, 4, 2, 2, c.max_pages, BF16, **{**dict(p=0.5), **kw})
+    path = make()
+    q, k, v = (t.cuda() for t in _path_inputs(c, 2, 3))
+    pages, sums = c.cache.pages.clone(), c.cache.ksum.clone()
+    wide = torch.zeros(2, 4 * 64 + 4, dtype=BF16, device="cuda")
+    flat = torch.zeros(2 * 4 * 64 + 8, dtype=BF16, device="cuda")
+    for bad in (wide[:, :256].unflatten(1, (4, 64)),                                 # row stride of 520 bytes
+                q.transpose(0, 1).contiguous().transpose(0, 1),                      # a row's heads lie apart
+                flat[1:513].view(2, 4, 64), path.out, q.cpu()):
+        with pytest.raises((ValueError, TypeError)):
+            path(c.batch, bad, k, v)
+    claims = F.KV4Batch(c.table, c.batch.kv_len, c.batch.cu, 500)
+    with pytest.raises(ValueError):
+        path(claims, q, k, v)
+    for kw in (dict(p=0.0), dict(p=1.5), dict(p=math.nan), dict(k_min=0), dict(scale=-1.0), dict(scale=math.inf)):
+        with pytest.raises(ValueError):
+            make(**kw)
+    assert torch.equal(pages, c.cache.pages) and torch.equal(sums, c.cache.ksum)
+    # a larger max_q that asks for no other kernel is none of its business
+    want = path(c.batch, q, k, v).clone()
+    assert torch.equal(want, path(F.KV4Batch(c.table, c.batch.kv_len, c.batch.cu, 4), q, k, v))
+
+
 def test_no_rows():
     c = Case([100], [1], 1, 64, 64, seed=26)
     e = torch.empty((0, 1, 64), dtype=BF16, device="cuda")
