@@ -128,7 +128,7 @@ __device__ __forceinline__ uint32_t quantize8(const Raw8<T>& raw, const Divisor&
   c = fmaf(fmaf(-c, 6.f, m), 0.166666672f, c);
   scale = float_to_e4m3(fminf(c, 448.f));     // 448 where an infinite m has made c a NaN
   const float s = e4m3_to_float(scale);
-  const float r = reciprocal(s);
+  const float r = scale == 0u ? 0.f : reciprocal(s);   // codes 0 where the scale is
   const float2 r2 = make_float2(r, r), s2 = make_float2(-s, -s);
   float q[8];
 #pragma unroll
@@ -138,7 +138,7 @@ __device__ __forceinline__ uint32_t quantize8(const Raw8<T>& raw, const Divisor&
     q[i] = d.x;
     q[i + 1] = d.y;
   }
-  return scale == 0u ? 0u : pack_e2m1x8(q);
+  return pack_e2m1x8(q);
 }
 
 // Adds eight stored values, in units of 2^-10, to integer sums. A value is a whole number
