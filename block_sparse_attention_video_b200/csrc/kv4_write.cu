@@ -128,7 +128,9 @@ __device__ __forceinline__ uint32_t quantize8(const Raw8<T>& raw, const Divisor&
   c = fmaf(fmaf(-c, 6.f, m), 0.166666672f, c);
   scale = float_to_e4m3(fminf(c, 448.f));     // 448 where an infinite m has made c a NaN
   const float s = e4m3_to_float(scale);
-  const float r = scale == 0u ? 0.f : reciprocal(s);   // codes 0 where the scale is
+  // Codes of zero where the scale is. (Some come out as minus zero; to make them plus costs 2% of the
+  // kernel: 9,360 tokens x 40 scaled heads 76.3 to 78.2 us.)
+  const float r = scale == 0u ? 0.f : reciprocal(s);
   const float2 r2 = make_float2(r, r), s2 = make_float2(-s, -s);
   float q[8];
 #pragma unroll

@@ -408,7 +408,7 @@ FVATTN_API fvattn_status fvattn_lvsa_lists(int B, int H, const fvattn_grid* grid
  * Quantization of 16 channels: x = fp32(input) / k_scale[h] (one correctly rounded fp32
  * division; none without k_scale); scale = the nearest E4M3 to min(max |x| / 6, 448);
  * code = the nearest E2M1 to x / scale, ties to the even code, at most 6 in magnitude;
- * codes 0 where scale is 0. Inputs must be finite (an infinity is stored as the largest
+ * codes of zero where scale is 0. The sign of a zero is unspecified. Inputs must be finite (an infinity is stored as the largest
  * value, a NaN as some value).
  * ksum[s][h][c] (int32) is the sum over a full page's tokens of the stored keys without
  * k_scale, in units of 2^-10 (every stored value is a whole number of them, so the sum is
