@@ -263,16 +263,13 @@ class KV4Path:
             raise ValueError(f"{rows} rows of {batch.B} sequences with {batch.max_pages} pages do not fit the path "
                              f"({self.max_rows}, {self.max_batch}, {self.max_pages})")
         # all of it before the first call writes into the cache (which looks at k and v itself)
-        if q.shape[1:] != self.out.shape[1:] or q.dtype != self.out.dtype:
-            raise ValueError(f"q is {tuple(q.shape)} {q.dtype}, the path's rows are {tuple(self.out.shape[1:])} "
-                             f"{self.out.dtype}")
-        _, heads, stride, _ = _rows(q, "q", self.cache.device, self.H_q, self.cache.d)
-        at, es, row = q.data_ptr(), q.element_size(), heads * self.cache.d
+        _, heads, stride, _ = _rows(q, "q", self.cache.device, self.H_q, self.cache.d, self.out.dtype)
+        at, out, es, row = q.data_ptr(), self.out.data_ptr(), q.element_size(), heads * self.cache.d
         if at % 16:
             raise ValueError("q must be 16-byte aligned")
-        if at < self.out.data_ptr() + rows * row * es and self.out.data_ptr() < at + ((rows - 1) * stride + row) * es:
+        if at < out + rows * row * es and out < at + ((rows - 1) * stride + row) * es:
             raise ValueError("q overlaps the path's output")
-        if batch.max_q > self.max_rows:              # more rows than there are: the attention's kernel for many may need more
+        if batch.max_q > self.max_rows:              # claimed, not there: the kernel for many rows may need more workspace
             need = fvattn_kv4_workspace_bytes(FVATTN_OP_KV4_ATTN, self.cache, batch, rows, self.H_q)
             if need > self.ws_attn.numel():
                 raise ValueError(f"the batch's max_q {batch.max_q} does not fit the path's {self.max_rows} rows")
