@@ -947,6 +947,29 @@ def test_captured_step_follows_the_lengths():
         assert torch.equal(got, want), kv
 
 
+def test_captured_step_past_the_tables_end():
+    """A captured step replayed until its stream no longer fits its table row: the cache keeps what it held."""
+    c = Case([126], [1], 2, 64, 64, seed=66, Hq=4)
+    c.table = c.table[:, :2].contiguous()
+    batch = F.KV4Batch(c.table, c.batch.kv_len, c.batch.cu, 1)
+    path = F.KV4Path(c.cache, 4, 1, 1, 2, BF16, p=0.9)
+    q, k, v = (t.cuda() for t in _path_inputs(c, 1, 4))
+    path(batch, q, k, v)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        path(batch, q, k, v)
+        batch.kv_len.add_(1)
+    for n in range(126, 133):
+        for t, s in zip((q, k, v), _path_inputs(c, 1, n)):
+            t.copy_(s)
+        graph.replay()
+        bad = [F.fvattn_workspace_status(ws) != F.FVATTN_OK for ws in (path.ws_append, path.ws_select, path.ws_attn)]
+        assert bad == [n > 128] * 3, n
+        if n == 128:
+            pages, sums = c.cache.pages.clone(), c.cache.ksum.clone()
+    assert torch.equal(pages, c.cache.pages) and torch.equal(sums, c.cache.ksum)
+
+
 def test_two_calls_at_once_and_repeats_are_bit_identical():
     c = Case([3000, 1700], [1, 1], 2, 128, 64, seed=23, Hq=8)
     d = Case([700, 900], [100, 130], 1, 64, 128, seed=24, Hq=4)
