@@ -661,8 +661,9 @@ size_t chunk_part_bytes(int d, int grid);
 cudaError_t launch_chunk(const AttnParams& P, int d, int grid, cudaStream_t st);
 
 // Where the 128-row tiles of kv4_chunk.cu take over (the fp32 path and lists stay here). Measured
-// at d 128, 8 KV heads, 16 sequences of up to 16k: 20 rows 286 us here and 307 there, 40 rows
-// 411 and 314; one sequence of 32k, 12 heads: 17 rows 62 and 83, 40 rows 91 and 86.
+// at d 128 in us, with units of sixteen rows here / there:
+//   16 sequences of 8k to 16k, 8 KV heads: 9 rows 125/246, 20 rows 181/247, 32 rows 231/248, 40 rows 280/248
+//   one sequence of 32k, 12 KV heads: 9 rows 51/83, 20 rows 66/83, 32 rows 70/84, 40 rows 95/84
 static bool many_rows(int max_q, int G) { return static_cast<long long>(max_q) * G > 32; }
 
 // Bytes of the flags, two a block (here) or four (kMaxChunkBlocks); cleared before a captured call.
@@ -703,7 +704,8 @@ cudaError_t launch_attn(const Cache& c, const Batch& bt, const void* q, long lon
   P.left = reinterpret_cast<unsigned long long*>(ws);
   P.part = reinterpret_cast<float*>(ws + attn_ws_clear());
   if (bf16 && !kv_idx && many_rows(max_q, P.G)) return launch_chunk(P, d, min(kMaxChunkBlocks, num_sms), st);
-  // Up to eight query rows a unit, or sixteen.
+  // Up to eight query rows a unit, or sixteen. The calls measured above do not bear this border out:
+  // with units of eight they take 73, 128, 176, 209 and 38, 48, 61, 71 us.
   const bool few = (kv_idx ? P.G : static_cast<long long>(max_q) * P.G) <= 8;
 #define FVATTN_KV4(T, HD) (few ? launch_stream<T, HD, 1>(P, num_sms, st) : launch_stream<T, HD, 2>(P, num_sms, st))
   if (bf16) return d == 128 ? FVATTN_KV4(__nv_bfloat16, 128) : FVATTN_KV4(__nv_bfloat16, 64);

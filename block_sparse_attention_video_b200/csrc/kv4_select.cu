@@ -9,8 +9,9 @@
 // pairs share every page's sum, which is converted to fp64 once for all of them. The floor of
 // a call of many rows is the fp64 units (d multiply-adds a pair and page, 64 a clock and
 // SM), of single tokens HBM (4 d bytes a page); what bounds both is the latency of one
-// block's chain (look-up, scores, softmax, search: a third of it each of the last three), so
-// loads go out several at a time and, in large grids, three blocks share an SM.
+// block's chain (780 rows over 591 pages: a sixth look-up, two fifths scores, a sixth softmax, a
+// third search and list), so loads go out several at a time and, in large grids, three blocks
+// share an SM.
 //   1. scores: fp64 tensor products of 8 pairs x 8 pages x 4 channels. q lies in shared memory;
 //      a page's sums are loaded straight into the operand's lanes (the order of channels in
 //      a dot product is free: lane t of a quad takes channels 16 i + 4 t .. + 3, 16 bytes).

@@ -86,7 +86,8 @@ class KV4Cache:
 class KV4Batch:
     """The sequences of a call: ``table`` [B, max_pages], ``kv_len`` [B] and ``cu`` [B+1], all int32
     CUDA tensors, and ``max_q``, the most rows any of them has. The tensors stay the batch's for its
-    lifetime; their contents may change."""
+    lifetime; their contents may change. Lengths and row starts are checked on the device, where they
+    are used (``fvattn_workspace_status``)."""
 
     def __init__(self, table, kv_len, cu, max_q):
         for t, name in ((table, "table"), (kv_len, "kv_len"), (cu, "cu")):
@@ -225,8 +226,10 @@ class KV4Path:
     """One attention layer's step over a KV4Cache with buffers allocated once.
 
     ``__call__(batch, q, k, v)`` writes the rows' k and v into the cache, chooses the pages of every
-    row (``p`` < 1) and attends; ``p=None`` attends the whole cache. At most ``max_rows`` rows a call;
-    the returned output is the path's buffer, overwritten by the next call."""
+    row (``p``, ``k_min``) and attends; ``p=None`` attends the whole cache. Choosing is for few rows a
+    sequence (tokens, drafts): lists are read row by row, and for a chunk's rows attending the whole
+    cache is faster. At most ``max_rows`` rows a call; the returned output is the path's buffer,
+    overwritten by the next call. What the path refuses it refuses before anything is written."""
 
     def __init__(self, cache: KV4Cache, H_q, max_rows, max_batch, max_pages, dtype, p=None, k_min=1, causal=True,
                  scale=None):
